@@ -561,4 +561,6 @@ int mxq_version(void);
 }
 #endif
 
+#include "mxq_decode.h"   /* few-row products, the NVFP4 cache and attention over it */
+
 #endif /* MXQ_H */

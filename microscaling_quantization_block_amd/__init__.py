@@ -5,6 +5,9 @@ library's HIP kernels.  PyTorch supplies device memory and the current stream.
 The names and arguments follow the C ABI in include/mxq.h:
     mx_quantize, nvfp4_quantize, mx_dequantize, mx_gemm, mx_swiglu,
     mx_gemm_set_tile
+and, for the decode step (decode.py, include/mxq_decode.h):
+    nvfp4_gemv, nvfp4_gemv_swiglu, NVFP4Cache, nvfp4_cache_append,
+    nvfp4_attention
 Outputs the caller does not pass are allocated here with torch (the library
 itself never allocates).  Every call is asynchronous on the current stream.
 
@@ -22,7 +25,9 @@ __all__ = ["Format", "Block", "GScale", "Round", "Layout", "Operand", "MXQError"
            "nvfp4_quantize_rowcol", "fp8bw_quantize",
            "fp8bw_quantize_f32",
            "mx_dequantize", "mx_gemm", "mx_gemm_swiglu", "mx_gemm_swiglu_nvfp4",
-           "mx_swiglu", "mx_gemm_set_tile", "library_path", "lib"]
+           "mx_swiglu", "mx_gemm_set_tile", "library_path", "lib",
+           "NVFP4Cache", "nvfp4_gemv", "nvfp4_gemv_swiglu", "nvfp4_cache_append", "nvfp4_attention",
+           "nvfp4_attention_workspace"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libmxq.so")
@@ -510,3 +515,7 @@ def mx_gemm_set_tile(tile):
     (0..8, as listed at mx_gemm_set_tile in include/mxq.h), or restore the
     measured choice with -1."""
     _check(lib().mx_gemm_set_tile(int(tile)))
+
+
+from .decode import (NVFP4Cache, nvfp4_attention, nvfp4_attention_workspace,  # noqa: E402
+                     nvfp4_cache_append, nvfp4_gemv, nvfp4_gemv_swiglu)

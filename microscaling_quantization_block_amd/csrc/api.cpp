@@ -7,12 +7,19 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include "api_common.h"
 #include "mxq.h"
 #include "mxq_kernels.h"
 
 namespace {
 
 thread_local char g_err[512] = "";
+
+hipStream_t S(void* s) { return reinterpret_cast<hipStream_t>(s); }
+
+}  // namespace
+
+namespace mxq {
 
 mxq_status fail(mxq_status s, const char* fmt, ...) {
   va_list ap;
@@ -32,11 +39,12 @@ mxq_status hip_status(hipError_t e, const char* what) {
   return ok();
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+}  // namespace mxq
 
-hipStream_t S(void* s) { return reinterpret_cast<hipStream_t>(s); }
-
-}  // namespace
+using mxq::aligned16;
+using mxq::fail;
+using mxq::hip_status;
+using mxq::ok;
 
 extern "C" {
 

@@ -1,0 +1,91 @@
+// Host-side launchers of the few-row products and of the 4-bit cache
+// (internal to the library).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mxq.h"
+
+namespace mxq {
+
+struct GemvArgs {
+  const uint16_t* x;
+  int64_t ld_x, x_rows;
+  const uint8_t* w;             // packed codes, group g at w + g * w_group
+  int64_t ld_w, w_group;        // bytes
+  const uint8_t* scales;        // group g at scales + g * s_group
+  int64_t s_group;
+  const float* gs;              // one per group
+  int64_t M, N, K;              // N: output columns (SwiGLU: the weight has 2 N rows)
+  uint16_t* y;
+  int64_t ld_y;
+  int num_groups;               // 0: dense
+  const int32_t* offsets;
+  const int32_t* row_index;
+};
+enum GemvScales { GS_ROW = 0, GS_MFMA = 1, GS_TILE = 2 };
+hipError_t launch_nvfp4_gemv(const GemvArgs& a, GemvScales layout, bool swiglu, hipStream_t st);
+
+// The pages of an NVFP4 cache (mxq_cache), by value.
+struct CacheArgs {
+  uint8_t *kc, *ks, *vc, *vs;   // codes, block scales
+  float *kg, *vg;               // second scales
+  int64_t pages, pc, psc, pg;   // page strides: code bytes, scale bytes, second scales
+  int H, D, P_log2;
+  const int32_t* table;         // [B, width], ld entries a row
+  int64_t ld_table, width;
+  const int32_t* seq_lens;
+  const int32_t* q_offsets;     // [B + 1], or nullptr: one token per request
+  int64_t B;
+};
+
+struct AppendArgs {
+  CacheArgs c;
+  const uint16_t *k, *v;
+  int64_t T, k_token, k_head, v_token, v_head;    // strides, elements
+  uint16_t *k_dq, *v_dq;        // [T, H, D], or nullptr
+};
+hipError_t launch_cache_append(const AppendArgs& a, hipStream_t st);
+
+struct AttnArgs {
+  CacheArgs c;
+  const uint16_t* q;
+  int64_t T, q_token, q_head;   // strides, elements
+  int Hq, G;                    // G = Hq / H query heads share a KV head
+  float scale_log2;             // scale * log2(e)
+  int64_t window;               // 0: none
+  uint16_t* out;
+  int64_t o_token, o_head;
+  float* lse;                   // [T, Hq], or nullptr
+  // partial results of the splits (splits > 1): normalized rows [splits, T * Hq, D] and
+  // their log2 sums [splits, T * Hq]
+  float *part_o, *part_lse;
+  int splits;
+};
+// How a call is cut: column tiles of 16 * nq * wq (query, head) pairs, an upper
+// bound of their number, and the splits of the context.
+struct AttnPlan {
+  int nq, wq, splits;
+  int64_t tiles;
+};
+inline AttnPlan plan_attention(int64_t B, int64_t T, int H, int G, int D, int64_t max_context, bool ragged) {
+  AttnPlan p;
+  // columns of an average request: a few fit one or two tiles of a wave, and
+  // the waves share the context; many are spread over the waves
+  const int64_t cols = (T + B - 1) / B * G;
+  p.nq = cols > 16 && D <= 128 ? 2 : 1;
+  p.wq = cols > 32 ? 4 : 1;
+  const int64_t ct = 16 * p.nq * p.wq;
+  p.tiles = ragged ? T * G / ct + B : B * ((G + ct - 1) / ct);
+  // enough workgroups for two per compute unit, each split at least 256 tokens
+  const int64_t wgs = p.tiles * H;
+  int64_t s = (512 + wgs - 1) / wgs;
+  const int64_t cap = (max_context + 255) / 256;
+  s = s > cap ? cap : s;
+  p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  return p;
+}
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st);
+
+}  // namespace mxq
