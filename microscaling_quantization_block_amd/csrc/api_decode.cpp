@@ -117,6 +117,8 @@ mxq_status cache_args(const char* fn, const mxq_cache* cache, const int32_t* blo
   const int64_t rows = (int64_t)cache->num_heads * P;
   if (cache->code_stride < rows * (D / 2) || cache->scale_stride < rows * (D / 16) || cache->gscale_stride < rows)
     return fail(MXQ_EINVAL, "%s: a page stride is smaller than a page", fn);
+  if (cache->code_stride >= I31 || cache->scale_stride >= I31 || cache->gscale_stride >= I31 / 4)
+    return fail(MXQ_EUNSUPPORTED, "%s: a page stride must be below 2 GiB", fn);
   if (!aligned16(cache->k_codes) || !aligned16(cache->v_codes) || !aligned16(cache->k_gscales) ||
       !aligned16(cache->v_gscales) || !aligned(cache->k_scales, 4) || !aligned(cache->v_scales, 4) ||
       cache->code_stride % 16 || cache->scale_stride % 4 || cache->gscale_stride % 4 || !aligned(block_table, 4) ||

@@ -33,6 +33,7 @@ namespace mxq {
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int FEW_WAVES = 4;                   // waves of a workgroup with few columns
 constexpr int TILE = 32;                       // tokens of one step of a wave
@@ -104,7 +105,13 @@ struct LaneOffsets {
 struct TilePages {
   int p[2];
 };
-__device__ __forceinline__ TilePages tile_pages(const CacheArgs& cc, const int32_t* table, int tile) {
+// The table is read through the constant address space: the scalar cache
+// then, whatever else the kernel stores (nothing writes the table meanwhile).
+typedef const int32_t __attribute__((address_space(4))) * ScalarTable;
+__device__ __forceinline__ ScalarTable scalar_table(const CacheArgs& cc, int b) {
+  return (ScalarTable)(uintptr_t)(cc.table + (int64_t)b * cc.ld_table);
+}
+__device__ __forceinline__ TilePages tile_pages(const CacheArgs& cc, ScalarTable table, int tile) {
   TilePages r;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -305,6 +312,28 @@ __device__ __forceinline__ int2 chunk_tiles(const Unit& u, const Reach& r) {
 
 // ---------------------------------------------------------------------- columns
 
+// A query row in FP16: its elements times 2^e, the largest then in [2^13, 2^14).
+// cs is the factor of a logit (log2) per unit of that product.  It is kept
+// positive (maxima are taken before it is applied): its sign goes to q, and
+// where it vanishes, q does.
+__device__ __forceinline__ int query_exponent(uint32_t amax, float scale_log2, float& cs, float& sign) {
+  const int e = amax ? 13 - ((int)(amax >> 7) - 127) : 0;
+  cs = __builtin_ldexpf(fabsf(scale_log2), -e);
+  sign = scale_log2 < 0.0f ? -1.0f : 1.0f;
+  if (!(cs > 0.0f)) cs = 1.0f, sign = 0.0f;
+  return e;
+}
+__device__ __forceinline__ f16x8 query_fragment(uint4 w, int e, float sign) {
+  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+  f16x8 q;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    q[2 * i] = (_Float16)(sign * __builtin_ldexpf(bf16_lo(ww[i]), e));
+    q[2 * i + 1] = (_Float16)(sign * __builtin_ldexpf(bf16_hi(ww[i]), e));
+  }
+  return q;
+}
+
 // The query columns of a wave and their running statistics.
 template <int D, int NQ>
 struct Columns {
@@ -347,21 +376,10 @@ __device__ __forceinline__ void load_columns(const AttnArgs& a, const Unit& u, i
     }
     amax = umax(amax, lane_xor_u32(amax, 16));
     amax = umax(amax, lane_xor_u32(amax, 32));
-    const int e = amax ? 13 - ((int)(amax >> 7) - 127) : 0;
-    // the factor of a logit is kept positive (the maximum is taken before it
-    // is applied): its sign goes to q, and where it vanishes, q does
-    o.cs[n] = __builtin_ldexpf(fabsf(a.scale_log2), -e);
-    float sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
-    if (!(o.cs[n] > 0.0f)) o.cs[n] = 1.0f, sign = 0.0f;
+    float sign;
+    const int e = query_exponent(amax, a.scale_log2, o.cs[n], sign);
 #pragma unroll
-    for (int j2 = 0; j2 < KF; ++j2) {
-      const uint32_t ww[4] = {w[j2].x, w[j2].y, w[j2].z, w[j2].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o.q[n][j2][2 * i] = (_Float16)(sign * __builtin_ldexpf(bf16_lo(ww[i]), e));
-        o.q[n][j2][2 * i + 1] = (_Float16)(sign * __builtin_ldexpf(bf16_hi(ww[i]), e));
-      }
-    }
+    for (int j2 = 0; j2 < KF; ++j2) o.q[n][j2] = query_fragment(w[j2], e, sign);
     o.m[n] = NEG_INF;
     o.limit[n] = NEG_INF;
     o.mu[n] = BASE;
@@ -427,46 +445,33 @@ __device__ __forceinline__ bool move_maxima(Columns<D, NQ>& o, const f32x4 (*x)[
   return true;
 }
 
-// Writes the columns' rows (normalized, in acc) or the unit's partial rows.
-// l: the sums against 2^(BASE - m cs).
-template <int D, int NQ, int CT>
-__device__ __forceinline__ void store_columns(const AttnArgs& a, const Unit& u, int64_t pu, int h, int col, int c, int g,
-                                              const Columns<D, NQ>& o, const float* m, const float* l) {
-  constexpr int ND = D / 16;
-  // (no global store comes before this point: page numbers are read through
-  // the scalar cache, which the compiler allows only to memory it sees untouched)
-  if (u.ct == 0 && u.chunk == 0 && h == 0 && threadIdx.x == 0 && a.target)
-    a.part_index[u.b] = make_int2((int)u.base, u.chunks);
-  // lane (c, g) holds, for its column, the values ND (4 g + i) + d
+// Writes N neighbouring values of a column's normalized row, from value `at`
+// on: to the output, or to the unit's partial row pr.
+template <int D, int N>
+__device__ __forceinline__ void store_run(const AttnArgs& a, const Unit& u, int64_t pr, int64_t row, int at,
+                                          const float* v) {
+  if (u.chunks > 1) {
+    float* p = a.part_o + pr * D + at;
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    if (!o.have[n]) continue;
-    const float lse2 = l[n] > 0.0f ? m[n] - BASE + __builtin_amdgcn_logf(l[n]) : NEG_INF;   // log2
-    if (u.chunks > 1) {
-      const int64_t pr = pu * CT + col + 16 * n + c;
-      if (g == 0) a.part_lse[pr] = lse2;
-      if (l[n] > 0.0f)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int d = 0; d < ND; d += 4)
-            *reinterpret_cast<f32x4*>(&a.part_o[pr * D + ND * (4 * g + i) + d]) =
-                f32x4{o.acc[n][d][i], o.acc[n][d + 1][i], o.acc[n][d + 2][i], o.acc[n][d + 3][i]};
-    } else {
-      const int64_t tq = o.row[n] / a.Hq, head = o.row[n] - tq * a.Hq;
-      uint16_t* out = a.out + tq * a.o_token + head * a.o_head;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int d = 0; d < ND; d += 4) {
-          uint2 w;
-          w.x = f32x2_to_bf16x2(o.acc[n][d][i], o.acc[n][d + 1][i]);
-          w.y = f32x2_to_bf16x2(o.acc[n][d + 2][i], o.acc[n][d + 3][i]);
-          *reinterpret_cast<uint2*>(out + ND * (4 * g + i) + d) = w;
-        }
-      if (a.lse && g == 0) a.lse[o.row[n]] = lse2 * 0.693147180559945309f;
-    }
+    for (int d = 0; d < N; d += 2) *reinterpret_cast<float2*>(p + d) = make_float2(v[d], v[d + 1]);
+    return;
   }
+  const int64_t tq = row / a.Hq, head = row - tq * a.Hq;
+  uint16_t* out = a.out + tq * a.o_token + head * a.o_head + at;
+#pragma unroll
+  for (int d = 0; d < N; d += 2) *reinterpret_cast<uint32_t*>(out + d) = f32x2_to_bf16x2(v[d], v[d + 1]);
+}
+// The log sum of a column; m: its maximum as a logit (log2), l: its sum
+// against 2^(BASE - m).
+__device__ __forceinline__ void store_lse(const AttnArgs& a, const Unit& u, int64_t pr, int64_t row, float m, float l) {
+  const float lse2 = l > 0.0f ? m - BASE + __builtin_amdgcn_logf(l) : NEG_INF;   // log2
+  if (u.chunks > 1) a.part_lse[pr] = lse2;
+  else if (a.lse) a.lse[row] = lse2 * 0.693147180559945309f;
+}
+// The join finds a request's units by this.
+__device__ __forceinline__ void store_index(const AttnArgs& a, const Unit& u, int h) {
+  if (a.target && u.ct == 0 && u.chunk == 0 && h == 0 && threadIdx.x == 0)
+    a.part_index[u.b] = make_int2((int)u.base, u.chunks);
 }
 
 // ------------------------------------------------------------- a few columns
@@ -592,7 +597,7 @@ __global__ __launch_bounds__(256, D <= 128 && NQ == 1 ? 3 : 2) void attention_fe
   const int h = blockIdx.x % cc.H, uid = blockIdx.x / cc.H;   // a unit's KV heads are neighbours
   Unit u;
   if (!find_unit(a, uid, CT, lane, u)) return;
-  const int32_t* table = cc.table + (int64_t)u.b * cc.ld_table;
+  const ScalarTable table = scalar_table(cc, u.b);
   const int64_t col0 = (int64_t)u.ct * CT;
 
   Columns<D, NQ> o;
@@ -676,243 +681,388 @@ done:
 #pragma unroll
       for (int w = 0; w < FEW_WAVES - 1; ++w)
         o.acc[n][d] += *reinterpret_cast<const f32x4*>(&s_o[(((w * NQ + n) * ND + d) * 64 + lane) * 4]);
-  store_columns<D, NQ, CT>(a, u, (int64_t)uid * cc.H + h, h, 0, c, g, o, m, l);
+  store_index(a, u, h);
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    if (!o.have[n]) continue;
+    const int64_t pr = ((int64_t)uid * cc.H + h) * CT + 16 * n + c;
+    if (g == 0) store_lse(a, u, pr, o.row[n], m[n], l[n]);
+    // lane (c, g) holds, for its column, the values ND (4 g + i) + d
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v[ND];
+#pragma unroll
+      for (int d = 0; d < ND; ++d) v[d] = o.acc[n][d][i];
+      store_run<D, ND>(a, u, pr, o.row[n], ND * (4 * g + i), v);
+    }
+  }
 }
 
 // -------------------------------------------------------------- many columns
 //
-// The W waves of a workgroup hold different columns and share the tiles: each
-// tile's K and V are dequantized once, a share per wave, into LDS, as the
-// very fragments the matrix instruction reads (a fragment is 64 lanes times 16
-// bytes, written and read without bank conflicts).  LDS holds two phases of PH
-// tiles: while one is attended to, the next one is filled, tile by tile, and
-// a barrier separates them; inside a phase the waves drift apart, so that the
-// matrix work of one meets the exponentials of another.  V carries its second
-// scale here, V' = fp16(c fp16(s_b S_t 2^4 / Sref)), so that the weights are the
-// plain exponentials.
-constexpr int phase_tiles(int D) { return D <= 128 ? 4 : 2; }
+// The eight waves of a workgroup hold 32 columns each and share the tiles.  A
+// tile passes through LDS twice.  It arrives as it is stored, by loads that
+// write LDS themselves (one or two instructions of a wave per tile, up to three
+// phases ahead, which covers the latency of a page that no cache holds), and is
+// then dequantized once, a share per wave, into the very fragments the matrix
+// instruction reads (64 lanes times 16 bytes, no bank conflicts).  A phase is
+// PH tiles: in phase p the waves attend to the fragments of p, make those of
+// p + 1 and issue the loads of p + 3; one barrier ends it, and inside it they
+// drift apart, so that one wave's matrix work meets another's exponentials.
+//
+// The 32x32x16 instruction takes 32 tokens and 32 columns at a time: half the
+// instructions of the 16x16x32 form, and a lane holds one column.  Lane (c, hh)
+// = (lane % 32, lane / 32): for K token c, the D / 2 values from hh D / 2 on; for
+// V the D / 32 values from c D / 32 on of the tokens 16 kk + 4 hh + i and
+// 16 kk + 8 + 4 hh + i (i < 4), kk = 0, 1.  V carries its second scale here, V' =
+// fp16(c fp16(s_b S_t 2^4 / Sref)), so that the weights are the plain
+// exponentials.
 template <int D>
-constexpr int many_lds() { return 2 * phase_tiles(D) * ((D / 8) * 1024 + 128 + 4); }
+struct ManyLayout {
+  static constexpr int W = MANY_WAVES, CT = 32 * W;
+  static constexpr int PH = D <= 128 ? 2 : 1, RING = 4;         // tiles of a phase, phases of raw tiles
+  static constexpr int NK = D / 16, NV = D / 16, F = NK + NV;   // fragments of a tile
+  // a raw tile: codes [32, D / 2] of K, of V, scales [32, D / 16] of K, [D / 16, 32] of V, second scales
+  static constexpr int CODES = 16 * D, KS = 2 * CODES, VS = KS + 2 * D, KG = VS + 2 * D, VG = KG + 128, RAW = VG + 128;
+  static constexpr int RAW0 = 2 * PH * F * 1024, E0 = RAW0 + RING * PH * RAW, LDS = E0 + 2 * PH * 4;
+  // load instructions of a tile: 1 KiB of codes each, or 64 words of scales
+  static constexpr int CODE_JOBS = 2 * D / 64, JOBS = CODE_JOBS + (D + 64) / 64, JW = (JOBS + W - 1) / W;
+};
+// LDS row of V's row r: four neighbouring rows are rotated by r / 4, so that the
+// two lane halves, which read rows four apart, meet different banks.
+__device__ __forceinline__ int v_row(int r) { return (r & ~3) | ((r + (r >> 2)) & 3); }
 
-template <int D, int W>
-__global__ __launch_bounds__(64 * W, 2) void attention_many_kernel(AttnArgs a) {
-  constexpr int KF = D / 32, ND = D / 16, NQ = D <= 128 ? 2 : 1, CT = 16 * NQ * W;
-  constexpr int F = 2 * KF + ND;               // fragments of a tile
-  static_assert(W == 8, "a word of V codes is eight values, one per wave");
-  constexpr int PH = phase_tiles(D), SLOTS = 2 * PH;
-  extern __shared__ uint4 s_frag[];            // [slot][F][64]
-  f32x4* s_kg = reinterpret_cast<f32x4*>(s_frag + SLOTS * F * 64);   // [slot][8]: second scales of K
-  int* s_e = reinterpret_cast<int*>(s_kg + SLOTS * 8);               // [slot]: exponent of Sref of V'
+// A wave's part in loading the tiles: per lane a base address, and what a page
+// and a token in it add to that.
+struct TileLoad {
+  const uint8_t* base;
+  uint32_t page_stride, slot_stride;
+  int half;                     // of the tile
+  uint32_t lds;                 // uniform, inside the raw tile
+};
+template <int D>
+__device__ __forceinline__ TileLoad tile_load(const CacheArgs& cc, int h, int job, int lane) {
+  using Y = ManyLayout<D>;
+  const int64_t P = 1 << cc.P_log2;
+  TileLoad t;
+  if (job < Y::CODE_JOBS) {
+    const bool v = job >= Y::CODE_JOBS / 2;
+    const int q = v ? job - Y::CODE_JOBS / 2 : job;
+    const int i = 64 * q + lane, at = i / (D / 32), chunk = i % (D / 32);
+    const int r = v ? (at & ~3) | ((at - (at >> 2)) & 3) : at;  // the row that belongs there
+    t.base = (v ? cc.vc : cc.kc) + (h * P + (r & 15)) * (D / 2) + 16 * chunk;
+    t.page_stride = (uint32_t)cc.pc;
+    t.slot_stride = D / 2;
+    t.half = r >> 4;
+    t.lds = (v ? Y::CODES : 0) + 1024 * q;
+    return t;
+  }
+  const int q = job - Y::CODE_JOBS, w = 64 * q + lane;          // word w of the scales
+  t.lds = Y::KS + 256 * q;
+  t.page_stride = (uint32_t)cc.psc;
+  if (w < D / 2) {
+    const int r = w / (D / 64);
+    t.base = cc.ks + (h * P + (r & 15)) * (D / 16) + 4 * (w % (D / 64));
+    t.slot_stride = D / 16;
+    t.half = r >> 4;
+  } else if (w < D) {
+    const int i = w - D / 2;
+    t.base = cc.vs + ((int64_t)h * (D / 16) + (i >> 3)) * P + 4 * (i & 3);
+    t.slot_stride = 1;
+    t.half = (i >> 2) & 1;
+  } else {
+    const int i = w - D, r = i & 31;
+    t.base = reinterpret_cast<const uint8_t*>((i < 32 ? cc.kg : cc.vg) + h * P + (r & 15));
+    t.page_stride = (uint32_t)(4 * cc.pg);
+    t.slot_stride = 4;
+    t.half = r >> 4;
+  }
+  return t;
+}
+// Loads that write LDS at m0 + lane * size; no register receives them.
+__device__ __forceinline__ void load_lds16(const void* p, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void load_lds4(const void* p, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+// Waits until at most N of the wave's loads are in flight and for its LDS
+// accesses, then for the workgroup.
+template <int N>
+__device__ __forceinline__ void loads_barrier() {
+  static_assert(N < 64, "vmcnt");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
+}
+
+template <int D>
+__global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(AttnArgs a) {
+  using Y = ManyLayout<D>;
+  constexpr int W = Y::W, PH = Y::PH, NK = Y::NK, NV = Y::NV, F = Y::F, DT = D / 32;
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_many[];
   const CacheArgs& cc = a.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, g = lane >> 4;
+  const int c = lane & 31, hh = lane >> 5;
   const int h = blockIdx.x % cc.H, uid = blockIdx.x / cc.H;
   Unit u;
-  if (!find_unit(a, uid, CT, lane, u)) return;
-  const int32_t* table = cc.table + (int64_t)u.b * cc.ld_table;
-  const int64_t col_wg = (int64_t)u.ct * CT, col0 = col_wg + wave * 16 * NQ;
-
-  Columns<D, NQ> o;
-  load_columns(a, u, h, col0, c, g, o);
-  float l[NQ] = {};
-  const Reach wg = reach(a, u, col_wg, col_wg + CT), re = reach(a, u, col0, col0 + 16 * NQ);
+  if (!find_unit(a, uid, Y::CT, lane, u)) return;
+  const ScalarTable table = scalar_table(cc, u.b);
+  const int64_t col_wg = (int64_t)u.ct * Y::CT, col0 = col_wg + wave * 32, ncols = (int64_t)u.q_len * a.G;
+  const Reach wg = reach(a, u, col_wg, col_wg + Y::CT), re = reach(a, u, col0, col0 + 32);
   const int2 tiles = chunk_tiles(u, wg);
-  const int P = 1 << cc.P_log2;
 
-  // The wave's share of a tile, as loaded: KW fragments of K and VW of V.  Where
-  // there are fewer than waves (D = 64) the lower half of the waves makes those
-  // of K, the upper half those of V; every wave loads both, so that no load
-  // depends on a branch.
-  constexpr int KW = (2 * KF + W - 1) / W, VW = (ND + W - 1) / W;
-  constexpr bool HALVES = F == W;
-  const int first = HALVES ? wave % (W / 2) : wave;
-  uint32_t kw[KW], ksc[KW], vw[VW][8];
-  uint32_t vs[2];
-  f32x4 kg[2], vg[2];
-  const LaneOffsets<D> off(cc, c, g);
-  auto load = [&](const TilePages& tp, int tile) {
-    const int64_t head = (int64_t)h * P;
+  // loads: phase p into ring slot p % RING; two bits per tile say which halves have a page
+  // (a wave without a load of its own repeats the last one, the same bytes to
+  // the same place, so that every wave has JW in flight per tile)
+  TileLoad job[Y::JW];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int64_t page = tp.p[s] < 0 ? 0 : tp.p[s];
-      const uint32_t slot = (tile * TILE + 16 * s) & (P - 1);
-      kg[s] = __builtin_bit_cast(f32x4, load4(buffer_at(cc.kg + page * cc.pg + head), off.g, slot * 4));
-      vg[s] = __builtin_bit_cast(f32x4, load4(buffer_at(cc.vg + page * cc.pg + head), off.g, slot * 4));
-      vs[s] = load1(buffer_at(cc.vs + page * cc.psc + head * (D / 16)), off.vs, slot);
-      const auto vc = buffer_at(cc.vc + page * cc.pc + head * (D / 2));
+  for (int k = 0; k < Y::JW; ++k) job[k] = tile_load<D>(cc, h, min(wave + W * k, Y::JOBS - 1), lane);
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(s_many);
+  uint64_t ok = 0;                             // of tile t at bits 2 (t % 32)
+  TilePages pages[PH];                         // of the phase to be issued next
+  auto look_up = [&](int p) {
 #pragma unroll
-      for (int k = 0; k < VW; ++k)             // fragment first + W k: value first of word k
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vw[k][4 * s + i] = load1(vc, off.v + i * (D / 2), slot * (D / 2) + 4 * k);
-    }
-#pragma unroll
-    for (int k = 0; k < KW; ++k) {
-      const int id = first + W * k, s = id / KF;
-      const int p = s ? tp.p[1] : tp.p[0];
-      const int64_t page = p < 0 ? 0 : p;
-      const uint32_t slot = (tile * TILE + 16 * s) & (P - 1);
-      kw[k] = load1(buffer_at(cc.kc + page * cc.pc + head * (D / 2)), off.k, slot * (D / 2) + 4 * (id % KF));
-      ksc[k] = load1(buffer_at(cc.ks + page * cc.psc + head * (D / 16)), off.ks, slot * (D / 16));
-    }
+    for (int i = 0; i < PH; ++i) pages[i] = tile_pages(cc, table, tiles.x + p * PH + i);
   };
-  int e_next = -100;                           // of the tile that was dequantized last
-  auto dequantize = [&](const TilePages& tp, int tile, int slot) {
-    const bool inside = tile * TILE >= wg.begin && (tile + 1) * TILE <= wg.end && tp.p[0] >= 0 && tp.p[1] >= 0;
-    if (!inside) {
-      drop_unused(vg, vs, tp, tile, wg.begin, wg.end, g);
-    }
-    float smax = 0.0f;
+  look_up(0);
+  auto issue = [&](int p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) smax = fmaxf(smax, fmaxf(vg[0][i], vg[1][i]));
-    smax = max_groups(smax);
-    e_next = max(e_next, __builtin_amdgcn_readfirstlane((int)(__float_as_uint(smax) >> 23) - 126));
-    f16x2 sc[2][2];
+    for (int i = 0; i < PH; ++i) {
+      const int n = p * PH + i, tile = tiles.x + n;
+      TilePages tp = pages[i];
+      if (tile >= tiles.y) tp.p[0] = tp.p[1] = -1;              // keeps the number of loads in flight
+      ok &= ~(3ull << (2 * (n & 31)));
+      ok |= (uint64_t)((tp.p[0] >= 0) | (tp.p[1] >= 0) << 1) << (2 * (n & 31));
+      const int p0 = tp.p[0] < 0 ? 0 : tp.p[0], p1 = tp.p[1] < 0 ? 0 : tp.p[1];
+      const int s0 = (tile * TILE) & ((1 << cc.P_log2) - 1), s1 = (tile * TILE + 16) & ((1 << cc.P_log2) - 1);
+      const uint32_t raw = lds0 + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const mxq_f32x2 b0 = __builtin_amdgcn_cvt_pk_f32_fp8(vs[s], false), b1 = __builtin_amdgcn_cvt_pk_f32_fp8(vs[s], true);
-      const mxq_f32x2 p0 = {__builtin_ldexpf(b0.x * vg[s][0], 4 - e_next), __builtin_ldexpf(b0.y * vg[s][1], 4 - e_next)};
-      const mxq_f32x2 p1 = {__builtin_ldexpf(b1.x * vg[s][2], 4 - e_next), __builtin_ldexpf(b1.y * vg[s][3], 4 - e_next)};
-      sc[s][0] = __builtin_convertvector(p0, f16x2);
-      sc[s][1] = __builtin_convertvector(p1, f16x2);
-    }
-    if (!HALVES || wave < W / 2)
-#pragma unroll
-      for (int k = 0; k < KW; ++k) {
-        const int id = first + W * k;
-        const f16x8 fr = k_fragment(kw[k], e4m3_pair<false>(ksc[k] >> (ks_shift<D>(g) + 8 * (id % KF >> 1))).x);
-        s_frag[(slot * F + id) * 64 + lane] = __builtin_bit_cast(uint4, fr);
+      for (int k = 0; k < Y::JW; ++k) {
+        const TileLoad& t = job[k];
+        const uint8_t* p8 = t.base + (uint64_t)(uint32_t)(t.half ? p1 : p0) * t.page_stride +
+                            (uint32_t)(t.half ? s1 : s0) * t.slot_stride;
+        if (wave + W * k < Y::CODE_JOBS) load_lds16(p8, raw + t.lds);
+        else load_lds4(p8, raw + t.lds);
       }
-    if (!HALVES || wave >= W / 2)
+    }
+    look_up(p + 1);
+  };
+
+  // columns: lane (c, hh) holds column col0 + c; values hh D / 2 + 8 j of q
+  const bool have = col0 + c < ncols;
+  const int qi = have ? (int)((col0 + c) / a.G) : 0, hg = have ? (int)(col0 + c - (int64_t)qi * a.G) : 0;
+  const int pos = have ? u.L - u.q_len + qi : -1;
+  const int64_t low = (int64_t)pos - a.window;
+  const int lo = a.window && low > -1 ? (int)low : -1;
+  const int64_t tq = (int64_t)u.q_begin + qi, head = (int64_t)h * a.G + hg, row = tq * a.Hq + head;
+  f16x8 q[NK];
+  float cs;
+  {
+    const uint16_t* qp = a.q + tq * a.q_token + head * a.q_head + hh * (D / 2);
+    uint4 w[NK];
+    uint32_t amax = 0;
 #pragma unroll
-      for (int k = 0; k < VW; ++k) {
-        const int sh = 4 * first + v_shift<D>(c);
+    for (int j = 0; j < NK; ++j) {
+      w[j] = *reinterpret_cast<const uint4*>(qp + 8 * j);
+      amax = umax(amax, umax(umax(bf16x2_absmax_bits(w[j].x), bf16x2_absmax_bits(w[j].y)),
+                             umax(bf16x2_absmax_bits(w[j].z), bf16x2_absmax_bits(w[j].w))));
+    }
+    amax = umax(amax, lane_xor_u32(amax, 32));
+    float factor;
+    const int e = query_exponent(amax, a.scale_log2, cs, factor);
+#pragma unroll
+    for (int j = 0; j < NK; ++j) q[j] = query_fragment(w[j], e, factor);
+  }
+  issue(0);
+  issue(1);
+  issue(2);
+  f32x16 acc[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
+  float m = NEG_INF, limit = NEG_INF, mu = BASE, l = 0.0f;
+  int e_ref = -100, e_fill = -100;             // exponents of Sref: of the sums, of the fragments made last
+
+  int* s_e = reinterpret_cast<int*>(s_many + Y::E0);            // [2][PH]: of the fragments
+  auto ok_of = [&](int n) { return (int)(ok >> (2 * (n & 31))) & 3; };
+
+  auto fill = [&](int p, int i) {
+    const int n = p * PH + i, tile = tiles.x + n, valid = ok_of(n);
+    const uint8_t* raw = s_many + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW;
+    uint4* frag = reinterpret_cast<uint4*>(s_many) + ((p & 1) * PH + i) * F * 64 + lane;
+    // a token outside the range, or without a page, may hold any bytes: its V
+    // scales count as zero (and its logit as -inf)
+    const bool inside = tile * TILE >= wg.begin && (tile + 1) * TILE <= wg.end && valid == 3;
+    {
+      float s = reinterpret_cast<const float*>(raw + Y::VG)[c];
+      if (!inside) {
+        const int t = tile * TILE + c;
+        s = (t >= wg.begin) & (t < wg.end) & ((valid >> (c >> 4)) & 1) ? s : 0.0f;
+      }
+      const uint32_t top = wave_max_u32(__float_as_uint(s));
+      e_fill = max(e_fill, (int)(top >> 23) - 126);
+    }
+    if (wave == 0 && lane == 0) s_e[(p & 1) * PH + i] = e_fill;
+    // K: fragment j holds the values hh D / 2 + 8 j of token c
+    const int kfirst = NK >= W ? wave : wave % NK;
+    if (NK >= W || wave < NK)
+#pragma unroll
+      for (int k = 0; k < (NK + W - 1) / W; ++k) {
+        const int j = kfirst + W * k, word = hh * NK + j;       // of the token's codes
+        const uint32_t code = *reinterpret_cast<const uint32_t*>(raw + c * (D / 2) + 4 * word);
+        const uint32_t sc = raw[Y::KS + c * (D / 16) + (word >> 1)];
+        frag[64 * j] = __builtin_bit_cast(uint4, k_fragment(code, e4m3_pair<false>(sc).x));
+      }
+    if (NV >= W || wave >= NK)
+#pragma unroll
+      for (int k = 0; k < (NV + W - 1) / W; ++k) {
+        const int v = (NV >= W ? wave : wave - NK) + W * k, dt = v % DT, kk = v / DT;
+        const uint8_t* codes = raw + Y::CODES + (c * DT / 8) * 4;
+        const int sh = 4 * ((c * DT + dt) & 7);
         f16x8 fr;
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int b = 0; b < 2; ++b) {          // tokens r .. r + 3
+          const int r = 16 * kk + 8 * b + 4 * hh;
+          f32x4 vg = *reinterpret_cast<const f32x4*>(raw + Y::VG + 4 * r);
+          uint32_t vs = *reinterpret_cast<const uint32_t*>(raw + Y::VS + (c * DT / 16) * 32 + r);
+          if (!inside)
 #pragma unroll
-          for (int ip = 0; ip < 2; ++ip) {
-            // the pair's two codes into the low byte, whichever value of the word it is
-            const uint32_t ta = vw[k][4 * s + 2 * ip] >> sh, tb = vw[k][4 * s + 2 * ip + 1] >> sh;
-            const f16x2 p = fp4_pair<0>((ta & 15u) | ((tb & 15u) << 4)) * sc[s][ip];
-            fr[4 * s + 2 * ip] = p.x;
-            fr[4 * s + 2 * ip + 1] = p.y;
-          }
-        s_frag[(slot * F + 2 * KF + first + W * k) * 64 + lane] = __builtin_bit_cast(uint4, fr);
-      }
-    if (wave == 0 && c == 0) {
-      s_kg[slot * 8 + g] = kg[0];
-      s_kg[slot * 8 + 4 + g] = kg[1];
-      if (g == 0) s_e[slot] = e_next;
-    }
-  };
-  auto attend = [&](const TilePages& tp, int tile, int slot) {
-    const bool inside = tile * TILE >= re.all_begin && (tile + 1) * TILE <= re.all_end && tp.p[0] >= 0 && tp.p[1] >= 0;
-    // all of K's fragments are read before the first product and V's before the
-    // exponentials, which cover their latency
-    const uint4* frag = s_frag + slot * F * 64 + lane;
-    uint4 fr[2 * KF > ND ? 2 * KF : ND];
+            for (int t = 0; t < 4; ++t) {
+              const int at = tile * TILE + r + t;
+              const bool use = (at >= wg.begin) & (at < wg.end) & ((valid >> kk) & 1);
+              vg[t] = use ? vg[t] : 0.0f;
+              vs &= use ? 0xFFFFFFFFu : ~(0xFFu << (8 * t));
+            }
+          uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 2 * KF; ++j) fr[j] = frag[64 * j];
-    const f32x4 kgs[2] = {s_kg[slot * 8 + g], s_kg[slot * 8 + 4 + g]};
-    __builtin_amdgcn_sched_barrier(0);
-    f32x4 x[NQ][2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) x[n][s] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < KF; ++j)
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-          x[n][s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, fr[s * KF + j]), o.q[n][j],
-                                                           x[n][s], 0, 0, 0);
-#pragma unroll
-    for (int d = 0; d < ND; ++d) fr[d] = frag[64 * (2 * KF + d)];
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) x[n][s] *= kgs[s];
-      if (!inside) mask_logits(o, n, x[n], tp, tile, g);
-    }
-    float alpha[NQ];
-    if (move_maxima(o, x, alpha))
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        l[n] *= alpha[n];
-#pragma unroll
-        for (int d = 0; d < ND; ++d) o.acc[n][d] *= alpha[n];
-      }
-    f16x8 wf[NQ];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const mxq_f32x2 pair = {__builtin_amdgcn_exp2f(__builtin_fmaf(x[n][s][i], o.cs[n], o.mu[n])),
-                                  __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][s][i + 1], o.cs[n], o.mu[n]))};
-          l[n] += pair.x + pair.y;             // of this lane group's tokens
-          const f16x2 hp = __builtin_convertvector(pair, f16x2);
-          wf[n][4 * s + i] = hp.x;
-          wf[n][4 * s + i + 1] = hp.y;
+          for (int t = 0; t < 4; ++t)
+            w[t] = (*reinterpret_cast<const uint32_t*>(codes + v_row(r + t) * (D / 2)) >> sh) & 15u;
+          const mxq_f32x2 b0 = __builtin_amdgcn_cvt_pk_f32_fp8(vs, false), b1 = __builtin_amdgcn_cvt_pk_f32_fp8(vs, true);
+          const mxq_f32x2 f0 = {__builtin_ldexpf(b0.x * vg[0], 4 - e_fill), __builtin_ldexpf(b0.y * vg[1], 4 - e_fill)};
+          const mxq_f32x2 f1 = {__builtin_ldexpf(b1.x * vg[2], 4 - e_fill), __builtin_ldexpf(b1.y * vg[3], 4 - e_fill)};
+          const f16x2 p0 = fp4_pair<0>(w[0] | w[1] << 4) * __builtin_convertvector(f0, f16x2);
+          const f16x2 p1 = fp4_pair<0>(w[2] | w[3] << 4) * __builtin_convertvector(f1, f16x2);
+          fr[4 * b] = p0.x, fr[4 * b + 1] = p0.y, fr[4 * b + 2] = p1.x, fr[4 * b + 3] = p1.y;
         }
+        frag[64 * (NK + v)] = __builtin_bit_cast(uint4, fr);
+      }
+  };
+
+  auto attend = [&](int p, int i) {
+    const int n = p * PH + i, tile = tiles.x + n, valid = ok_of(n);
+    // V' of this tile may be on a larger Sref than the sums
+    const int e = __builtin_amdgcn_readfirstlane(s_e[(p & 1) * PH + i]);
+    if (e > e_ref) {
+      const float grow = __builtin_ldexpf(1.0f, e_ref - e);
+      e_ref = e;
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      const f16x8 vf = __builtin_bit_cast(f16x8, fr[d]);
+      for (int d = 0; d < DT; ++d) acc[d] *= grow;
+    }
+    if (tile * TILE >= re.end || (tile + 1) * TILE <= re.begin) return;
+    const uint4* frag = reinterpret_cast<const uint4*>(s_many) + ((p & 1) * PH + i) * F * 64 + lane;
+    const uint8_t* raw = s_many + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW;
+    // fragments are read eight at a time, V's first ones before the
+    // exponentials, which cover their latency
+    uint4 fr[8];
+    f32x16 x = {};
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) o.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf[n], o.acc[n][d], 0, 0, 0);
+    for (int j0 = 0; j0 < NK; j0 += 8) {
+#pragma unroll
+      for (int j = 0; j < 8 && j < NK; ++j) fr[j] = frag[64 * (j0 + j)];
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 8 && j < NK; ++j)
+        x = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, fr[j]), q[j0 + j], x, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 8 && j < NV; ++j) fr[j] = frag[64 * (NK + j)];
+    f32x4 kg[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) kg[b] = *reinterpret_cast<const f32x4*>(raw + Y::KG + 4 * (8 * b + 4 * hh));
+    __builtin_amdgcn_sched_barrier(0);
+    // element i of x: token 8 (i / 4) + 4 hh + i % 4
+#pragma unroll
+    for (int i2 = 0; i2 < 16; ++i2) x[i2] *= kg[i2 >> 2][i2 & 3];
+    if (!(tile * TILE >= re.all_begin && (tile + 1) * TILE <= re.all_end && valid == 3)) {
+#pragma unroll
+      for (int i2 = 0; i2 < 16; ++i2) {
+        const int t = tile * TILE + 8 * (i2 >> 2) + 4 * hh + (i2 & 3);
+        const int last = (valid >> (i2 >> 3)) & 1 ? pos : -1;
+        x[i2] = (t <= last) & (t > lo) ? x[i2] : NEG_INF;
+      }
+    }
+    float mx = x[0];
+#pragma unroll
+    for (int i2 = 1; i2 < 16; ++i2) mx = fmaxf(mx, x[i2]);
+    if (__any(mx > limit)) {
+      const uint32_t bits = __float_as_uint(mx);
+      const auto sw = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+      const float top = max2(m, max2(__uint_as_float(sw[0]), __uint_as_float(sw[1])));
+      const float mu_new = top == NEG_INF ? BASE : BASE - top * cs;
+      const float alpha = __builtin_amdgcn_exp2f(__builtin_fmaf(m, cs, mu_new - BASE));
+      m = top;
+      mu = mu_new;
+      limit = top == NEG_INF ? NEG_INF : top + HEADROOM / cs;
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) acc[d] *= alpha;
+    }
+    f16x8 wf[2];
+#pragma unroll
+    for (int i2 = 0; i2 < 16; i2 += 2) {
+      const mxq_f32x2 pair = {__builtin_amdgcn_exp2f(__builtin_fmaf(x[i2], cs, mu)),
+                              __builtin_amdgcn_exp2f(__builtin_fmaf(x[i2 + 1], cs, mu))};
+      l += pair.x + pair.y;                    // of this lane half's tokens
+      const f16x2 hp = __builtin_convertvector(pair, f16x2);
+      wf[i2 >> 3][i2 & 7] = hp.x;
+      wf[i2 >> 3][(i2 & 7) + 1] = hp.y;
+    }
+#pragma unroll
+    for (int v0 = 0; v0 < NV; v0 += 8) {
+      if (v0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) fr[j] = frag[64 * (NK + v0 + j)];
+      }
+#pragma unroll
+      for (int j = 0; j < 8 && j < NV; ++j)
+        acc[(v0 + j) % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, fr[j]),
+                                                                    wf[(v0 + j) / DT], acc[(v0 + j) % DT], 0, 0, 0);
     }
   };
 
-  if (tiles.x < tiles.y) {
-    // `filled`: tiles dequantized so far; the loads of the next one are in
-    // flight (behind the last tile they read some page, which stays unused)
-    int filled = tiles.x;
-    TilePages next = tile_pages(cc, table, filled);
-    load(next, filled);
-    auto fill = [&]() {
-      const TilePages far = tile_pages(cc, table, filled + 1);
-      dequantize(next, filled, (filled - tiles.x) % SLOTS);
-      ++filled;
-      next = far;
-      load(next, filled);
-    };
-    for (int i = 0; i < PH && filled < tiles.y; ++i) fill();
-    __syncthreads();
-    TilePages now = tile_pages(cc, table, tiles.x);
-    for (int tile = tiles.x; tile < tiles.y; ++tile) {
-      const TilePages after = tile_pages(cc, table, tile + 1);
-      const int slot = (tile - tiles.x) % SLOTS;
-      // V' of this tile may be on a larger Sref than the sums
-      const int e = __builtin_amdgcn_readfirstlane(s_e[slot]);
-      if (e > o.e_ref) {
-        const float grow = __builtin_ldexpf(1.0f, o.e_ref - e);
-        o.e_ref = e;
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int d = 0; d < ND; ++d) o.acc[n][d] *= grow;
+  const int count = tiles.y - tiles.x;
+  if (count > 0) {
+    const int phases = (count + PH - 1) / PH;
+    loads_barrier<2 * PH * Y::JW>();           // phase 0 is here
+    for (int i = 0; i < PH; ++i) fill(0, i);
+    loads_barrier<PH * Y::JW>();               // its fragments, and phase 1
+    for (int p = 0; p < phases; ++p) {
+      issue(p + 3);
+#pragma unroll 1
+      for (int i = 0; i < PH; ++i) {
+        if (p * PH + i < count) attend(p, i);
+        if (p + 1 < phases) fill(p + 1, i);
       }
-      if (tile * TILE < re.end && (tile + 1) * TILE > re.begin) attend(now, tile, slot);
-      if (filled < tiles.y) fill();
-      if ((tile - tiles.x) % PH == PH - 1) __syncthreads();
-      now = after;
+      loads_barrier<PH * Y::JW>();             // the fragments of p + 1, and phase p + 2
     }
   }
-  float m[NQ];
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    m[n] = o.m[n] * o.cs[n];
-    l[n] += __shfl_xor(l[n], 16, 64);
-    l[n] += __shfl_xor(l[n], 32, 64);
-    const float f = l[n] > 0.0f ? __builtin_ldexpf(1.0f / l[n], o.e_ref - 4) : 0.0f;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) o.acc[n][d] *= f;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");              // no load may write LDS after the workgroup has ended
+  {
+    const uint32_t bits = __float_as_uint(l);
+    const auto sw = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+    l = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
   }
-  store_columns<D, NQ, CT>(a, u, (int64_t)uid * cc.H + h, h, wave * 16 * NQ, c, g, o, m, l);
+  const float f = l > 0.0f ? __builtin_ldexpf(1.0f / l, e_ref - 4) : 0.0f;
+  store_index(a, u, h);
+  if (!have) return;
+  const int64_t pr = ((int64_t)uid * cc.H + h) * Y::CT + wave * 32 + c;
+  if (hh == 0) store_lse(a, u, pr, row, m * cs, l);
+  // the lane holds the values DT r + d of its column, r = 8 (i / 4) + 4 hh + i % 4
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float v[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) v[d] = acc[d][i] * f;
+    store_run<D, DT>(a, u, pr, row, DT * (8 * (i >> 2) + 4 * hh + (i & 3)), v);
+  }
 }
 
 // Joins the chunks of one (token, head): weights 2^(lse_s - lse).  RW waves
@@ -985,11 +1135,11 @@ template <int D>
 static hipError_t launch_attention_d(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   const dim3 grid((unsigned)(a.c.H * p.units));
   if (p.waves) {
-    constexpr int lds = many_lds<D>();
+    constexpr int lds = ManyLayout<D>::LDS;
     static std::atomic<uint32_t> done{0};
-    hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&attention_many_kernel<D, MANY_WAVES>), lds, done);
+    hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&attention_many_kernel<D>), lds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attention_many_kernel<D, MANY_WAVES>), grid, dim3(64 * MANY_WAVES), lds, st, a);
+    hipLaunchKernelGGL(attention_many_kernel<D>, grid, dim3(64 * MANY_WAVES), lds, st, a);
   } else if (p.nq == 1) {
     hipLaunchKernelGGL((attention_few_kernel<D, 1>), grid, dim3(256), 0, st, a);
   } else {

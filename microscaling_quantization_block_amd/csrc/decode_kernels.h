@@ -82,8 +82,8 @@ inline AttnPlan plan_attention(int64_t B, int64_t T, int H, int G, int D, int64_
   const int64_t cols = (T + B - 1) / B * G;
   const int nq_max = D <= 128 ? 2 : 1;
   p.waves = cols > 16 * nq_max ? MANY_WAVES : 0;
-  p.nq = p.waves ? nq_max : cols > 16 ? 2 : 1;
-  p.ct = 16 * p.nq * (p.waves ? p.waves : 1);
+  p.nq = cols > 16 ? 2 : 1;
+  p.ct = p.waves ? 32 * p.waves : 16 * p.nq;
   const int64_t tiles = ragged ? T * G / p.ct + B : B * ((G + p.ct - 1) / p.ct);
   // workgroups aimed at
   const int64_t want = p.waves ? 256 : 768;
