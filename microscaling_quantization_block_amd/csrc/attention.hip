@@ -707,8 +707,9 @@ done:
 // then dequantized once, a share per wave, into the very fragments the matrix
 // instruction reads (64 lanes times 16 bytes, no bank conflicts).  A phase is
 // PH tiles: in phase p the waves attend to the fragments of p, make those of
-// p + 1 and issue the loads of p + 3; one barrier ends it, and inside it they
-// drift apart, so that one wave's matrix work meets another's exponentials.
+// p + 1 and issue the loads of p + 3; one barrier ends it.  Of the two waves of
+// a SIMD one attends first and the other fills first, so that one's matrix
+// work meets the other's conversions.
 //
 // The 32x32x16 instruction takes 32 tokens and 32 columns at a time: half the
 // instructions of the 16x16x32 form, and a lane holds one column.  Lane (c, hh)
@@ -724,7 +725,7 @@ struct ManyLayout {
   static constexpr int NK = D / 16, NV = D / 16, F = NK + NV;   // fragments of a tile
   // a raw tile: codes [32, D / 2] of K, of V, scales [32, D / 16] of K, [D / 16, 32] of V, second scales
   static constexpr int CODES = 16 * D, KS = 2 * CODES, VS = KS + 2 * D, KG = VS + 2 * D, VG = KG + 128, RAW = VG + 128;
-  static constexpr int RAW0 = 2 * PH * F * 1024, E0 = RAW0 + RING * PH * RAW, LDS = E0 + 2 * PH * 4;
+  static constexpr int RAW0 = 2 * PH * F * 1024, LDS = RAW0 + RING * PH * RAW;
   // load instructions of a tile: 1 KiB of codes each, or 64 words of scales
   static constexpr int CODE_JOBS = 2 * D / 64, JOBS = CODE_JOBS + (D + 64) / 64, JW = (JOBS + W - 1) / W;
 };
@@ -809,31 +810,33 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
   const int64_t col_wg = (int64_t)u.ct * Y::CT, col0 = col_wg + wave * 32, ncols = (int64_t)u.q_len * a.G;
   const Reach wg = reach(a, u, col_wg, col_wg + Y::CT), re = reach(a, u, col0, col0 + 32);
   const int2 tiles = chunk_tiles(u, wg);
+  const int count = tiles.y - tiles.x;
 
-  // loads: phase p into ring slot p % RING; two bits per tile say which halves have a page
+  // loads: phase p into ring slot p % RING
   // (a wave without a load of its own repeats the last one, the same bytes to
   // the same place, so that every wave has JW in flight per tile)
   TileLoad job[Y::JW];
 #pragma unroll
   for (int k = 0; k < Y::JW; ++k) job[k] = tile_load<D>(cc, h, min(wave + W * k, Y::JOBS - 1), lane);
   const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(s_many);
-  uint64_t ok = 0;                             // of tile t at bits 2 (t % 32)
+  // which halves of the tiles have a page: two bits per tile, the current phase lowest
+  uint32_t ok = 0;
   TilePages pages[PH];                         // of the phase to be issued next
   auto look_up = [&](int p) {
 #pragma unroll
     for (int i = 0; i < PH; ++i) pages[i] = tile_pages(cc, table, tiles.x + p * PH + i);
   };
   look_up(0);
-  auto issue = [&](int p) {
+  const int page_mask = (1 << cc.P_log2) - 1;
+  auto issue = [&](int p, int ahead) {
 #pragma unroll
     for (int i = 0; i < PH; ++i) {
-      const int n = p * PH + i, tile = tiles.x + n;
+      const int tile = tiles.x + p * PH + i;
       TilePages tp = pages[i];
       if (tile >= tiles.y) tp.p[0] = tp.p[1] = -1;              // keeps the number of loads in flight
-      ok &= ~(3ull << (2 * (n & 31)));
-      ok |= (uint64_t)((tp.p[0] >= 0) | (tp.p[1] >= 0) << 1) << (2 * (n & 31));
-      const int p0 = tp.p[0] < 0 ? 0 : tp.p[0], p1 = tp.p[1] < 0 ? 0 : tp.p[1];
-      const int s0 = (tile * TILE) & ((1 << cc.P_log2) - 1), s1 = (tile * TILE + 16) & ((1 << cc.P_log2) - 1);
+      ok |= (uint32_t)((tp.p[0] >= 0) | (tp.p[1] >= 0) << 1) << (2 * (ahead * PH + i));
+      const int p0 = max(tp.p[0], 0), p1 = max(tp.p[1], 0);
+      const int s0 = (tile * TILE) & page_mask, s1 = (tile * TILE + 16) & page_mask;
       const uint32_t raw = lds0 + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW;
 #pragma unroll
       for (int k = 0; k < Y::JW; ++k) {
@@ -872,35 +875,40 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
 #pragma unroll
     for (int j = 0; j < NK; ++j) q[j] = query_fragment(w[j], e, factor);
   }
-  issue(0);
-  issue(1);
-  issue(2);
+  issue(0, 0);
+  issue(1, 1);
+  issue(2, 2);
   f32x16 acc[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
   float m = NEG_INF, limit = NEG_INF, mu = BASE, l = 0.0f;
   int e_ref = -100, e_fill = -100;             // exponents of Sref: of the sums, of the fragments made last
 
-  int* s_e = reinterpret_cast<int*>(s_many + Y::E0);            // [2][PH]: of the fragments
-  auto ok_of = [&](int n) { return (int)(ok >> (2 * (n & 31))) & 3; };
+  // ranges of tiles of the chunk: some token in reach of the wave's columns, every
+  // token in reach of all of them, every token inside the workgroup's range
+  const int any0 = re.begin / TILE - tiles.x, any1 = (re.end + TILE - 1) / TILE - tiles.x;
+  const int all0 = (re.all_begin + TILE - 1) / TILE - tiles.x, all1 = re.all_end / TILE - tiles.x;
+  const int in0 = (wg.begin + TILE - 1) / TILE - tiles.x, in1 = wg.end / TILE - tiles.x;
 
-  auto fill = [&](int p, int i) {
-    const int n = p * PH + i, tile = tiles.x + n, valid = ok_of(n);
+  // The exponent of Sref for phase p, whose tiles are there: a power of two
+  // above every second scale of V so far.
+  auto scale_of = [&](int p, int shift) {
+    const int i = PH == 2 ? hh : 0, n = p * PH + i, valid = (int)(ok >> (2 * (shift * PH + i))) & 3;
+    float v = reinterpret_cast<const float*>(s_many + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW + Y::VG)[c];
+    const int t = (tiles.x + n) * TILE + c;
+    v = (t >= wg.begin) & (t < wg.end) & (valid >> (c >> 4) & 1) ? v : 0.0f;
+    e_fill = max(e_fill, (int)(wave_max_u32(__float_as_uint(v)) >> 23) - 126);
+  };
+
+  // Makes the fragments of tile i of phase p.  A token outside the range, or
+  // without a page, may hold any bytes: its V scales count as zero (and its
+  // logit as -inf).
+  auto fill = [&](int p, int i, int shift) {
+    const int n = p * PH + i, tile = tiles.x + n, valid = (int)(ok >> (2 * (shift * PH + i))) & 3;
     const uint8_t* raw = s_many + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW;
     uint4* frag = reinterpret_cast<uint4*>(s_many) + ((p & 1) * PH + i) * F * 64 + lane;
-    // a token outside the range, or without a page, may hold any bytes: its V
-    // scales count as zero (and its logit as -inf)
-    const bool inside = tile * TILE >= wg.begin && (tile + 1) * TILE <= wg.end && valid == 3;
-    {
-      float s = reinterpret_cast<const float*>(raw + Y::VG)[c];
-      if (!inside) {
-        const int t = tile * TILE + c;
-        s = (t >= wg.begin) & (t < wg.end) & ((valid >> (c >> 4)) & 1) ? s : 0.0f;
-      }
-      const uint32_t top = wave_max_u32(__float_as_uint(s));
-      e_fill = max(e_fill, (int)(top >> 23) - 126);
-    }
-    if (wave == 0 && lane == 0) s_e[(p & 1) * PH + i] = e_fill;
+    const bool inside = (n >= in0) & (n < in1) & (valid == 3);
+    const float to_ref = __builtin_ldexpf(1.0f, 4 - e_fill);
     // K: fragment j holds the values hh D / 2 + 8 j of token c
     const int kfirst = NK >= W ? wave : wave % NK;
     if (NK >= W || wave < NK)
@@ -935,9 +943,10 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
 #pragma unroll
           for (int t = 0; t < 4; ++t)
             w[t] = (*reinterpret_cast<const uint32_t*>(codes + v_row(r + t) * (D / 2)) >> sh) & 15u;
-          const mxq_f32x2 b0 = __builtin_amdgcn_cvt_pk_f32_fp8(vs, false), b1 = __builtin_amdgcn_cvt_pk_f32_fp8(vs, true);
-          const mxq_f32x2 f0 = {__builtin_ldexpf(b0.x * vg[0], 4 - e_fill), __builtin_ldexpf(b0.y * vg[1], 4 - e_fill)};
-          const mxq_f32x2 f1 = {__builtin_ldexpf(b1.x * vg[2], 4 - e_fill), __builtin_ldexpf(b1.y * vg[3], 4 - e_fill)};
+          // the conversion applies the power of two
+          const mxq_f32x2 b0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(vs, to_ref, false);
+          const mxq_f32x2 b1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(vs, to_ref, true);
+          const mxq_f32x2 f0 = {b0.x * vg[0], b0.y * vg[1]}, f1 = {b1.x * vg[2], b1.y * vg[3]};
           const f16x2 p0 = fp4_pair<0>(w[0] | w[1] << 4) * __builtin_convertvector(f0, f16x2);
           const f16x2 p1 = fp4_pair<0>(w[2] | w[3] << 4) * __builtin_convertvector(f1, f16x2);
           fr[4 * b] = p0.x, fr[4 * b + 1] = p0.y, fr[4 * b + 2] = p1.x, fr[4 * b + 3] = p1.y;
@@ -947,16 +956,8 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
   };
 
   auto attend = [&](int p, int i) {
-    const int n = p * PH + i, tile = tiles.x + n, valid = ok_of(n);
-    // V' of this tile may be on a larger Sref than the sums
-    const int e = __builtin_amdgcn_readfirstlane(s_e[(p & 1) * PH + i]);
-    if (e > e_ref) {
-      const float grow = __builtin_ldexpf(1.0f, e_ref - e);
-      e_ref = e;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) acc[d] *= grow;
-    }
-    if (tile * TILE >= re.end || (tile + 1) * TILE <= re.begin) return;
+    const int n = p * PH + i, tile = tiles.x + n, valid = (int)(ok >> (2 * i)) & 3;
+    if ((n < any0) | (n >= any1) | (n >= count)) return;
     const uint4* frag = reinterpret_cast<const uint4*>(s_many) + ((p & 1) * PH + i) * F * 64 + lane;
     const uint8_t* raw = s_many + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW;
     // fragments are read eight at a time, V's first ones before the
@@ -981,7 +982,7 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
     // element i of x: token 8 (i / 4) + 4 hh + i % 4
 #pragma unroll
     for (int i2 = 0; i2 < 16; ++i2) x[i2] *= kg[i2 >> 2][i2 & 3];
-    if (!(tile * TILE >= re.all_begin && (tile + 1) * TILE <= re.all_end && valid == 3)) {
+    if ((n < all0) | (n >= all1) | (valid != 3)) {
 #pragma unroll
       for (int i2 = 0; i2 < 16; ++i2) {
         const int t = tile * TILE + 8 * (i2 >> 2) + 4 * hh + (i2 & 3);
@@ -1028,19 +1029,29 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
     }
   };
 
-  const int count = tiles.y - tiles.x;
   if (count > 0) {
     const int phases = (count + PH - 1) / PH;
+    const bool late = wave >= W / 2;
     loads_barrier<2 * PH * Y::JW>();           // phase 0 is here
-    for (int i = 0; i < PH; ++i) fill(0, i);
+    scale_of(0, 0);
+    for (int i = 0; i < PH; ++i) fill(0, i, 0);
     loads_barrier<PH * Y::JW>();               // its fragments, and phase 1
     for (int p = 0; p < phases; ++p) {
-      issue(p + 3);
-#pragma unroll 1
-      for (int i = 0; i < PH; ++i) {
-        if (p * PH + i < count) attend(p, i);
-        if (p + 1 < phases) fill(p + 1, i);
+      issue(p + 3, 3);
+      // V' of this phase may be on a larger Sref than the sums
+      if (e_fill > e_ref) {
+        const float grow = __builtin_ldexpf(1.0f, e_ref - e_fill);
+        e_ref = e_fill;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[d] *= grow;
       }
+      scale_of(p + 1, 1);
+#pragma unroll 1
+      for (int k = 0; k < 2 * PH; ++k) {
+        if (((k & 1) != 0) == late) attend(p, k >> 1);
+        else fill(p + 1, k >> 1, 1);           // behind the last phase: page 0, unused
+      }
+      ok >>= 2 * PH;
       loads_barrier<PH * Y::JW>();             // the fragments of p + 1, and phase p + 2
     }
   }
