@@ -6,14 +6,21 @@
 // binary32.  S leaves the sum and multiplies it once, in binary32; one
 // rounding to BF16 ends the chain.
 //
-// One workgroup owns 16 weight rows (with SwiGLU 16 gate rows and their up
-// rows) and all of K; its waves take 128-wide K chunks in turn and their
-// partial tiles meet in LDS, so there are many loads in flight for a
-// matrix with few rows and no second launch.  The weights are the left
-// operand: lane (r, g) = (lane % 16, lane / 16) reads 16 bytes, the codes
-// k0 + 32 g .. + 31 of row r, and feeds them to four matrix instructions
-// eight at a time; x is read in the same order, so k is permuted alike on
-// both sides and nothing is shuffled.
+// One workgroup owns 16 RT weight rows (with SwiGLU as many gate rows and
+// their up rows) and all of K; its waves take 256-wide K chunks in turn (a whole
+// 128-byte line of codes per row) and their partial tiles meet in LDS, so there
+// are many loads in flight for a matrix with few rows and no second launch.
+// The weights are the left operand: lane (c, g) = (lane % 16, lane / 16) reads
+// 32 bytes, the codes k0 + 64 g .. + 63 of row c, with their four scales in one
+// word, and feeds them to eight matrix instructions eight at a time; x is read
+// in the same order, so k is permuted alike on both sides and nothing is
+// shuffled.  RT > 1 because x comes through the caches: 16 rows of x are four
+// times the bytes of 16 rows of codes.
+//
+// Bound by memory: the codes are read once.  A chunk's loads are in flight
+// while the one before it is multiplied; no load in the loop depends on a
+// branch (lanes without a row of x read some row, whose column is dropped at
+// the end), so the waits count them.
 
 #include "mxq_device.h"
 #include "decode_kernels.h"
@@ -44,11 +51,13 @@ __device__ __forceinline__ int64_t gemv_scale_offset(int64_t row, int64_t b, int
   return scale_offset(row, b, B, SL == GS_MFMA);
 }
 
-template <int SL, bool SWI, int MT>
-__global__ __launch_bounds__(1024) void gemv_kernel(GemvArgs a) {
-  constexpr int R = SWI ? 2 : 1;
+// R tiles of 16 weight rows (with SwiGLU tile 2 t holds gate rows and tile
+// 2 t + 1 their up rows), MT tiles of 16 rows of x.
+template <int SL, bool SWI, int R, int MT>
+__global__ __launch_bounds__(R == 1 ? 1024 : 512) void gemv_kernel(GemvArgs a) {
+  constexpr int RT = SWI ? R / 2 : R;          // tiles of output columns
   extern __shared__ float red[];               // [waves][R][MT * 16 columns m][16 rows n]
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, nw = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   const int grp = blockIdx.y;
   int64_t m_begin = 0, m_end = a.M;
@@ -59,21 +68,23 @@ __global__ __launch_bounds__(1024) void gemv_kernel(GemvArgs a) {
     m_end = m_end > a.M ? a.M : m_end;
   }
   if (m_begin >= m_end) return;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, B = a.K >> 4;
-  const uint8_t* wrow[R];
-  const uint8_t* srow[R];
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * RT, B = a.K >> 4;
+  const int full = (int)(a.K >> 8), rest = (int)(a.K & 255);   // whole chunks, and what is left
+  // the lane's codes and scales of chunk 0; a chunk adds 128 bytes and 16 (MFMA: 512) bytes of scales
+  const uint8_t* wp[R];
+  const uint8_t* sp[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    int64_t row = n0 + c;
-    row = (row < a.N ? row : a.N - 1) + r * a.N;
-    wrow[r] = a.w + grp * a.w_group + row * a.ld_w;
-    srow[r] = a.scales + grp * a.s_group + gemv_scale_offset<SL>(row, 0, B);
+    int64_t row = n0 + (SWI ? r >> 1 : r) * 16 + c;
+    row = (row < a.N ? row : a.N - 1) + (SWI && (r & 1) ? a.N : 0);
+    wp[r] = a.w + grp * a.w_group + row * a.ld_w + 32 * g;
+    sp[r] = a.scales + grp * a.s_group + gemv_scale_offset<SL>(row, 0, B) + (SL == GS_MFMA ? 128 : 4) * g;
   }
+  constexpr int S_CHUNK = SL == GS_MFMA ? 512 : 16;
   const float S = a.gs[grp];
-  const int64_t chunks = (a.K + 127) >> 7;
 
   for (int64_t m0 = m_begin; m0 < m_end; m0 += 16 * MT) {
-    const uint16_t* xrow[MT];
+    const uint16_t* xp[MT];
     bool have[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -82,7 +93,7 @@ __global__ __launch_bounds__(1024) void gemv_kernel(GemvArgs a) {
       have[t] = m < m_end;
       if (have[t] && a.row_index) xr = a.row_index[m];
       have[t] = have[t] && xr >= 0 && xr < a.x_rows;
-      xrow[t] = a.x + (have[t] ? xr : 0) * a.ld_x;
+      xp[t] = a.x + (have[t] ? xr : 0) * a.ld_x + 64 * g;
     }
     f32x4 acc[R][MT];
 #pragma unroll
@@ -90,88 +101,323 @@ __global__ __launch_bounds__(1024) void gemv_kernel(GemvArgs a) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
 
-#pragma unroll 2
-    for (int64_t ch = wave; ch < chunks; ch += nw) {
-      const int64_t k = ch * 128 + g * 32, b = k >> 4;
-      // K % 16 == 0: a lane holds two blocks, one, or none
-      const int nb = b + 1 < B ? 2 : b < B ? 1 : 0;
-      uint4 w[R];
+    struct Chunk {
+      uint4 w[R][2], x[MT][8];
       uint32_t s[R];
+    };
+    auto load = [&](Chunk& k, int ch) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        w[r] = make_uint4(0, 0, 0, 0);
-        s[r] = 0;
-        const int64_t so = SL == GS_MFMA ? (b >> 2) * 128 + (b & 3) : b;
-        if (nb == 2) {
-          __builtin_memcpy(&w[r], wrow[r] + (k >> 1), 16);
-          uint16_t two;
-          __builtin_memcpy(&two, srow[r] + so, 2);
-          s[r] = two;
-        } else if (nb == 1) {
-          uint2 half;
-          __builtin_memcpy(&half, wrow[r] + (k >> 1), 8);
-          w[r].x = half.x;
-          w[r].y = half.y;
-          s[r] = srow[r][so];
-        }
+        __builtin_memcpy(&k.w[r][0], wp[r] + (int64_t)ch * 128, 16);
+        __builtin_memcpy(&k.w[r][1], wp[r] + (int64_t)ch * 128 + 16, 16);
+        __builtin_memcpy(&k.s[r], sp[r] + (int64_t)ch * S_CHUNK, 4);
       }
-      uint4 x[MT][4];
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[t][j] = make_uint4(0, 0, 0, 0);
-          if (have[t] && (j >> 1) < nb) x[t][j] = *reinterpret_cast<const uint4*>(xrow[t] + k + 8 * j);
-        }
+        for (int j = 0; j < 8; ++j) k.x[t][j] = *reinterpret_cast<const uint4*>(xp[t] + (int64_t)ch * 256 + 8 * j);
+    };
+    auto multiply = [&](const Chunk& k) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float s0 = e4m3_to_f32(s[r] & 0xFF), s1 = e4m3_to_f32(s[r] >> 8);
-        const uint32_t ww[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+        const uint32_t ww[8] = {k.w[r][0].x, k.w[r][0].y, k.w[r][0].z, k.w[r][0].w,
+                                k.w[r][1].x, k.w[r][1].y, k.w[r][1].z, k.w[r][1].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8 av = e2m1x8_to_bf16(ww[j], j < 2 ? s0 : s1);
+        for (int j = 0; j < 8; ++j) {
+          const bf16x8 av = e2m1x8_to_bf16(ww[j], e4m3_to_f32((k.s[r] >> (8 * (j >> 1))) & 0xFF));
 #pragma unroll
           for (int t = 0; t < MT; ++t)
-            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8, x[t][j]),
-                                                                acc[r][t], 0, 0, 0);
+            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8, k.x[t][j]), acc[r][t],
+                                                                0, 0, 0);
         }
       }
+    };
+
+    // the wave's whole chunks: wave, wave + nw, ...
+    if (full > wave) {
+      Chunk k[2];
+      const int last = wave + (full - wave - 1) / nw * nw;
+      load(k[0], wave);
+      int ch = wave;
+      while (true) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          load(k[1 - h], min(ch + nw, last));  // behind the last one: that again
+          multiply(k[h]);
+          ch += nw;
+          if (ch > last) goto done;
+        }
+      }
+    }
+  done:
+    // what is left of K: a lane holds up to four blocks
+    if (rest && wave == full % nw) {
+      const int nb = min(max((rest >> 4) - 4 * g, 0), 4);
+      Chunk k;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint8_t* w = wp[r] + (int64_t)full * 128;
+        const uint8_t* s = sp[r] + (int64_t)full * S_CHUNK;
+        k.s[r] = 0;
+        uint2 d[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          d[b] = make_uint2(0, 0);
+          if (b < nb) {
+            __builtin_memcpy(&d[b], w + 8 * b, 8);
+            k.s[r] |= (uint32_t)s[b] << (8 * b);
+          }
+        }
+        k.w[r][0] = make_uint4(d[0].x, d[0].y, d[1].x, d[1].y);
+        k.w[r][1] = make_uint4(d[2].x, d[2].y, d[3].x, d[3].y);
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          k.x[t][j] = make_uint4(0, 0, 0, 0);
+          if ((j >> 1) < nb) k.x[t][j] = *reinterpret_cast<const uint4*>(xp[t] + (int64_t)full * 256 + 8 * j);
+        }
+      multiply(k);
     }
     // lane (c, g) holds column m = c, rows n = 4 g .. + 3 of each tile
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int t = 0; t < MT; ++t)
-        *reinterpret_cast<f32x4*>(&red[(((wave * R + r) * MT + t) * 16 + c) * 16 + 4 * g]) = acc[r][t];
+        *reinterpret_cast<f32x4*>(&red[(((wave * R + r) * MT + t) * 16 + c) * 16 + 4 * g]) =
+            have[t] ? acc[r][t] : f32x4{0, 0, 0, 0};
     __syncthreads();
-    const int64_t cols = m_end - m0 < 16 * MT ? m_end - m0 : 16 * MT;
-    for (int i = threadIdx.x; i < (int)cols * 16; i += blockDim.x) {
-      const int m = i >> 4, n = i & 15;
-      float v[R];
+    const int cols = (int)(m_end - m0 < 16 * MT ? m_end - m0 : 16 * MT);
+    for (int i = threadIdx.x; i < cols * 16 * RT; i += blockDim.x) {
+      const int n = i & 15, rt = (i >> 4) % RT, m = i / (16 * RT);
+      float v[2];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        v[r] = 0.0f;
-        for (int w = 0; w < nw; ++w) v[r] += red[((w * R + r) * MT * 16 + m) * 16 + n];
-        v[r] *= S;
+      for (int e = 0; e < (SWI ? 2 : 1); ++e) {
+        const int r = SWI ? 2 * rt + e : rt;
+        v[e] = 0.0f;
+        for (int w = 0; w < nw; ++w) v[e] += red[((w * R + r) * MT * 16 + m) * 16 + n];
+        v[e] *= S;
       }
       // SwiGLU on the binary32 sums: silu(g) u = g / (1 + exp(-g)) u
-      const float out = SWI ? v[0] / (1.0f + expf(-v[0])) * v[R - 1] : v[0];
-      if (n0 + n < a.N) a.y[(m0 + m) * a.ld_y + n0 + n] = (uint16_t)f32x2_to_bf16x2(out, 0.0f);
+      const float out = SWI ? v[0] / (1.0f + expf(-v[0])) * v[1] : v[0];
+      const int64_t col = n0 + rt * 16 + n;
+      if (col < a.N) a.y[(m0 + m) * a.ld_y + col] = (uint16_t)f32x2_to_bf16x2(out, 0.0f);
     }
     __syncthreads();
   }
 }
 
+template <int SL, bool SWI, int R, int MT>
+static hipError_t launch_gemv_as(const GemvArgs& a, hipStream_t st) {
+  constexpr int RT = SWI ? R / 2 : R;
+  // a wave per chunk, as far as there is room
+  const int chunks = (int)((a.K + 255) >> 8), most = R == 1 ? 16 : 8, per = (chunks + most - 1) / most;
+  const int nw = (chunks + per - 1) / per;
+  const dim3 grid((unsigned)((a.N + 16 * RT - 1) / (16 * RT)), (unsigned)(a.num_groups ? a.num_groups : 1));
+  const size_t lds = (size_t)nw * R * MT * 256 * sizeof(float);
+  hipLaunchKernelGGL((gemv_kernel<SL, SWI, R, MT>), grid, dim3(64 * nw), lds, st, a);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ a few rows
+//
+// For up to three rows of x or so per matrix the matrix instruction has little
+// to do, and its operand layout reads 16 rows at once, 16 bytes each, which
+// the memory path takes apart.  Here the lanes lie along K: a lane holds 32
+// codes of a row, 16 bytes, and a load of a wave is one kilobyte of one row
+// (or of 64 / LPR rows where K is short).  A wave reads 16 such pieces of
+// neighbouring rows, all in flight at once, and multiplies them with its part
+// of x, which stays in registers: codes to BF16 pairs (exact), v_dot2 in
+// binary32, the two blocks' sums times their E4M3 scales, then a sum over the
+// lanes: over the 16 of a group piece by piece, after which lane c keeps piece
+// c, and over the groups for all 16 pieces at once.  Waves take different
+// rows, and where K is longer than 32 LPR different parts of K, which meet in
+// LDS.
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int DOT_ITEMS = 16;
+constexpr int MMX = 2;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+// Sum over the 16 lanes of a group, in every one of them.
+__device__ __forceinline__ float sum16(float v) {
+  v = dpp_add<0xB1>(v);                        // quads: neighbours, pairs
+  v = dpp_add<0x4E>(v);
+  v = dpp_add<0x141>(v);                       // mirrors: halves of 16, 16
+  return dpp_add<0x140>(v);
+}
+// Sum over the lane groups of a row (LPR / 16 of them).
+template <int LPR>
+__device__ __forceinline__ float sum_groups(float v) {
+  if (LPR >= 32) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  if (LPR >= 64) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  return v;
+}
+
+// Eight codes times eight values of x (as BF16 pairs).
+__device__ __forceinline__ float dot8(uint32_t w, uint4 x, float acc) {
+  const bf16x2 c[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1),
+                       __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3)};
+  const uint32_t xx[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    acc = __builtin_amdgcn_fdot2_f32_bf16(c[i], __builtin_bit_cast(bf16x2, xx[i]), acc, false);
+  return acc;
+}
+
+// MM rows of x at a time; ks waves of a workgroup share a row's K.
+template <int SL, bool SWI, int LPR, int MM>
+__global__ __launch_bounds__(512, 2) void gemv_dot_kernel(GemvArgs a, int ks) {
+  constexpr int ITEMS = DOT_ITEMS, RPL = 64 / LPR;             // rows of a load
+  constexpr int ROWS = ITEMS * RPL, OUT = SWI ? ROWS / 2 : ROWS;   // of a wave: weight rows, output columns
+  constexpr int RUN = SWI ? ITEMS / 2 : ITEMS;                 // neighbouring rows of a lane
+  __shared__ float part[8][ROWS * MM];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kpart = wave % ks, rpart = wave / ks, rs = (int)(blockDim.x >> 6) / ks;
+  const int grp = blockIdx.y;
+  int64_t m_begin = 0, m_end = a.M;
+  if (a.num_groups) {
+    m_begin = a.offsets[grp];
+    m_end = a.offsets[grp + 1];
+    m_begin = m_begin < 0 ? 0 : m_begin;
+    m_end = m_end > a.M ? a.M : m_end;
+  }
+  if (m_begin >= m_end) return;
+  const int64_t B = a.K >> 4;
+  const int64_t n0 = ((int64_t)blockIdx.x * rs + rpart) * OUT;   // first output column of the wave
+  // the lane's codes: k0 .. k0 + 31, of which those from `from` on count (the
+  // last piece of a K that is no multiple of 32 overlaps the one before)
+  const int64_t from = ((int64_t)kpart * LPR + lane % LPR) * 32;
+  const int64_t k0 = from + 32 <= a.K ? from : a.K - 32, b0 = k0 >> 4;
+  uint4 w[ITEMS];
+  uint32_t s[ITEMS];                           // the lane's two scales, in the low half
+  const uint8_t* scales = a.scales + grp * a.s_group;
+#pragma unroll
+  for (int r = 0; r < ITEMS / RUN; ++r) {      // SwiGLU: gate rows, then up rows
+    // rows behind the last one are read as rows before it, and not written
+    const int64_t first = n0 + (int64_t)(lane / LPR) * RUN;
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      const int64_t row = (first + i < a.N ? first + i : a.N - 1) + r * a.N;
+      __builtin_memcpy(&w[r * RUN + i], a.w + grp * a.w_group + row * a.ld_w + (k0 >> 1), 16);
+      if (SL == GS_ROW) {
+        uint16_t two;
+        __builtin_memcpy(&two, scales + row * B + b0, 2);
+        s[r * RUN + i] = two;
+      }
+    }
+    if (SL == GS_TILE) {                       // one tile row: N and the first row are multiples of RUN
+      uint16_t two;
+      __builtin_memcpy(&two, scales + (((first < a.N ? first : 0) + r * a.N) >> 4) * B + b0, 2);
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) s[r * RUN + i] = two;
+    }
+    if (SL == GS_MFMA) {                       // four rows' words of four blocks are neighbours
+      const int64_t row = (first < a.N ? first : 0) + r * a.N;
+      const uint8_t* p = scales + ((row >> 5) * (B >> 2) + (b0 >> 2)) * 128 + (row & 31) * 4;
+#pragma unroll
+      for (int i = 0; i < RUN; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+        const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[r * RUN + i + j] = word[j] >> (8 * (b0 & 3));
+      }
+    }
+  }
+  const float S = a.gs[grp];
+  for (int64_t m0 = m_begin; m0 < m_end; m0 += MM) {
+    uint4 x[MM][4];
+#pragma unroll
+    for (int m = 0; m < MM; ++m) {
+      int64_t xr = m0 + m;
+      bool have = xr < m_end;
+      if (have && a.row_index) xr = a.row_index[xr];
+      have = have && xr >= 0 && xr < a.x_rows;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[m][j] = make_uint4(0, 0, 0, 0);
+        const int64_t k = k0 + 8 * j;
+        if (have && k >= from && from < a.K) x[m][j] = *reinterpret_cast<const uint4*>(a.x + xr * a.ld_x + k);
+      }
+    }
+    float sums[MM] = {};
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      // (keeps the conversions inside the loop over m0: outside they would take
+      // four times the registers)
+      asm("" : "+v"(w[i].x), "+v"(w[i].y), "+v"(w[i].z), "+v"(w[i].w), "+v"(s[i]));
+      const float s0 = e4m3_to_f32(s[i] & 0xFF), s1 = e4m3_to_f32((s[i] >> 8) & 0xFF);
+#pragma unroll
+      for (int m = 0; m < MM; ++m) {
+        const float d0 = dot8(w[i].y, x[m][1], dot8(w[i].x, x[m][0], 0.0f));
+        const float d1 = dot8(w[i].w, x[m][3], dot8(w[i].z, x[m][2], 0.0f));
+        const float v = sum16(__builtin_fmaf(d0, s0, d1 * s1));
+        sums[m] = (lane & 15) == i ? v : sums[m];
+      }
+    }
+    // lane c of a row's first group: weight row RUN (lane / LPR) + c % RUN of the gate or up rows
+#pragma unroll
+    for (int m = 0; m < MM; ++m) {
+      sums[m] = sum_groups<LPR>(sums[m]);
+      const int i = lane & 15;
+      if (lane % LPR < 16) part[wave][(i / RUN * OUT + lane / LPR * RUN + i % RUN) * MM + m] = sums[m];
+    }
+    __syncthreads();
+    const int cols = (int)(m_end - m0 < MM ? m_end - m0 : MM);
+    for (int t = threadIdx.x; t < rs * OUT * cols; t += blockDim.x) {
+      const int n = t % OUT, r = t / OUT % rs, m = t / (OUT * rs);
+      float v[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int e = 0; e < (SWI ? 2 : 1); ++e) {
+        for (int k = 0; k < ks; ++k) v[e] += part[r * ks + k][(n + e * OUT) * MM + m];
+        v[e] *= S;
+      }
+      const float out = SWI ? v[0] / (1.0f + expf(-v[0])) * v[1] : v[0];
+      const int64_t col = ((int64_t)blockIdx.x * rs + r) * OUT + n;
+      if (col < a.N) a.y[(m0 + m) * a.ld_y + col] = (uint16_t)f32x2_to_bf16x2(out, 0.0f);
+    }
+    __syncthreads();
+  }
+}
+
+template <int SL, bool SWI, int LPR, int MM>
+static hipError_t launch_dot_as(const GemvArgs& a, hipStream_t st) {
+  const int ks = (int)((a.K + 32 * LPR - 1) / (32 * LPR)), rs = ks > 4 ? 1 : ks > 2 ? 2 : 8 / ks;
+  const int64_t out = (int64_t)rs * DOT_ITEMS * (64 / LPR) / (SWI ? 2 : 1);
+  const dim3 grid((unsigned)((a.N + out - 1) / out), (unsigned)(a.num_groups ? a.num_groups : 1));
+  hipLaunchKernelGGL((gemv_dot_kernel<SL, SWI, LPR, MM>), grid, dim3(64 * ks * rs), 0, st, a, ks);
+  return hipGetLastError();
+}
+
+template <int SL, bool SWI>
+static hipError_t launch_dot_sl(const GemvArgs& a, bool one, hipStream_t st) {
+  if (a.K <= 512) return one ? launch_dot_as<SL, SWI, 16, 1>(a, st) : launch_dot_as<SL, SWI, 16, MMX>(a, st);
+  if (a.K <= 1024) return one ? launch_dot_as<SL, SWI, 32, 1>(a, st) : launch_dot_as<SL, SWI, 32, MMX>(a, st);
+  return one ? launch_dot_as<SL, SWI, 64, 1>(a, st) : launch_dot_as<SL, SWI, 64, MMX>(a, st);
+}
+
 template <int SL, bool SWI>
 static hipError_t launch_gemv_sl(const GemvArgs& a, hipStream_t st) {
-  // waves of a workgroup: about four K chunks each, 16 at most
-  const int64_t chunks = (a.K + 127) >> 7;
-  const int nw = chunks >= 64 ? 16 : chunks >= 32 ? 8 : chunks >= 8 ? 4 : chunks >= 2 ? 2 : 1;
-  const int groups = a.num_groups ? a.num_groups : 1;
-  const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)groups);
-  const size_t lds = (size_t)nw * (SWI ? 2 : 1) * 256 * sizeof(float);
-  hipLaunchKernelGGL((gemv_kernel<SL, SWI, 1>), grid, dim3(64 * nw), lds, st, a);
-  return hipGetLastError();
+  const int64_t groups = a.num_groups ? a.num_groups : 1;
+  const int64_t rows = (a.M + groups - 1) / groups;            // of x, per matrix
+  const int64_t tiles = (a.N + 15) / 16 * groups;
+  if (rows <= 3 && a.K >= 32 && a.K <= 16384) return launch_dot_sl<SL, SWI>(a, rows == 1, st);
+  if (rows > 16) return launch_gemv_as<SL, SWI, 2, 2>(a, st);
+  if (tiles >= 2048) return launch_gemv_as<SL, SWI, 4, 1>(a, st);
+  if (SWI || tiles >= 1024) return launch_gemv_as<SL, SWI, 2, 1>(a, st);
+  if constexpr (!SWI) return launch_gemv_as<SL, SWI, 1, 1>(a, st);
+  return hipErrorInvalidValue;                 // not reached
 }
 
 hipError_t launch_nvfp4_gemv(const GemvArgs& a, GemvScales layout, bool swiglu, hipStream_t st) {
