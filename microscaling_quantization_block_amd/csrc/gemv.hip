@@ -278,7 +278,7 @@ __device__ __forceinline__ float dot8(uint32_t w, uint4 x, float acc) {
 
 // MM rows of x at a time; ks waves of a workgroup share a row's K.
 template <int SL, bool SWI, int LPR, int MM>
-__global__ __launch_bounds__(512, 2) void gemv_dot_kernel(GemvArgs a, int ks) {
+__global__ __launch_bounds__(512, MM == 1 ? 4 : 3) void gemv_dot_kernel(GemvArgs a, int ks) {
   constexpr int ITEMS = DOT_ITEMS, RPL = 64 / LPR;             // rows of a load
   constexpr int ROWS = ITEMS * RPL, OUT = SWI ? ROWS / 2 : ROWS;   // of a wave: weight rows, output columns
   constexpr int RUN = SWI ? ITEMS / 2 : ITEMS;                 // neighbouring rows of a lane
@@ -393,7 +393,7 @@ __global__ __launch_bounds__(512, 2) void gemv_dot_kernel(GemvArgs a, int ks) {
 
 template <int SL, bool SWI, int LPR, int MM>
 static hipError_t launch_dot_as(const GemvArgs& a, hipStream_t st) {
-  const int ks = (int)((a.K + 32 * LPR - 1) / (32 * LPR)), rs = ks > 4 ? 1 : ks > 2 ? 2 : 8 / ks;
+  const int ks = (int)((a.K + 32 * LPR - 1) / (32 * LPR)), rs = ks > 4 ? 1 : 4 / ks;
   const int64_t out = (int64_t)rs * DOT_ITEMS * (64 / LPR) / (SWI ? 2 : 1);
   const dim3 grid((unsigned)((a.N + out - 1) / out), (unsigned)(a.num_groups ? a.num_groups : 1));
   hipLaunchKernelGGL((gemv_dot_kernel<SL, SWI, LPR, MM>), grid, dim3(64 * ks * rs), 0, st, a, ks);
