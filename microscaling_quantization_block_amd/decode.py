@@ -3,14 +3,15 @@ rows with NVFP4 weights, the paged NVFP4 cache, and attention over it.
 
 Like the rest of the package: argument marshalling and host checks only,
 outputs and workspaces the caller does not pass are allocated with torch, and
-every call is asynchronous, on the current stream of its tensors' device
-unless a stream is given."""
+every call is asynchronous, on the current stream of its tensors' device or on
+the one given as stream=."""
 
 import ctypes
+import functools
 
 import torch
 
-from . import Operand, _Operand, _check, _check_2d, lib
+from . import Block, Operand, _Operand, _check, _check_2d, lib
 
 __all__ = ["NVFP4Cache", "nvfp4_gemv", "nvfp4_gemv_swiglu", "nvfp4_cache_append", "nvfp4_attention",
            "nvfp4_attention_workspace"]
@@ -50,21 +51,48 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _launch(device, stream, fn, *args):
-    """Calls fn(*args, stream) with `device` current (a launch goes to the
-    current device, whatever its pointers are)."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        _check(fn(*args, s.cuda_stream))
+# The raw handle of a device's current stream and the current device: a decode
+# step is many short calls, and the objects around these cost as much as a call.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _launch(device, fn, *args):
+    """Calls fn(*args, stream) on the device's current stream, with `device`
+    current (a launch goes to the current device, whatever its pointers are)."""
+    if device.index == _current_device():
+        status = fn(*args, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
-            s = torch.cuda.current_stream(device) if stream is None else stream
-            _check(fn(*args, s.cuda_stream))
+            status = fn(*args, _raw_stream(device.index))
+    if status:
+        _check(status)
+
+
+def _takes_stream(call):
+    """Adds stream=None.  With a stream the whole call runs with it current, so
+    that what the call allocates (the workspace above all, which goes back to
+    the allocator at once) belongs to that stream."""
+    @functools.wraps(call)
+    def wrapped(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.device != stream.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return wrapped
+
+
+def _is(t, dtype, dim, device):
+    """A tensor of that kind on that device (host tensors never: device is a GPU)."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == dim and t.device == device
 
 
 def _check_tensor(t, name, dtype, dim, device):
+    if _is(t, dtype, dim, device) and t.is_cuda:
+        return
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim:
         raise TypeError(f"{name} must be a {dim}-D {dtype} tensor")
     if not t.is_cuda or t.device != device:
@@ -72,19 +100,24 @@ def _check_tensor(t, name, dtype, dim, device):
 
 
 def _check_index(t, name, n, device):
-    _check_tensor(t, name, torch.int32, 1, device)
-    if not t.is_contiguous() or t.numel() != n:
+    if not _is(t, torch.int32, 1, device):
+        _check_tensor(t, name, torch.int32, 1, device)
+    if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} entries")
 
 
-def _room(name, t, need, step):
-    if t.numel() < need:
-        raise ValueError(f"{name} holds {t.numel()} values, {need} {step}")
+def _room(name, t, need):
+    """At least `need` bytes of storage from the tensor's first element on (rows may be strided)."""
+    have = t.numel() * t.element_size()
+    if have < need:
+        have = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+        if have < need:
+            raise ValueError(f"{name} holds {have} bytes, {need} are read")
 
 
 # ------------------------------------------------------------- few-row products
 
-def _gemv(fn, x, w, M, N, K, weight_rows, out, group_row_offsets, x_row_index, stream):
+def _gemv(fn, x, w, M, N, K, weight_rows, out, group_row_offsets, x_row_index):
     _check_2d(x, torch.bfloat16, "x")
     dev = x.device
     if not isinstance(w, Operand):
@@ -101,42 +134,47 @@ def _gemv(fn, x, w, M, N, K, weight_rows, out, group_row_offsets, x_row_index, s
         _check_index(x_row_index, "x_row_index", M, dev)
     elif x.shape[0] != M:
         raise ValueError(f"x has {x.shape[0]} rows, M is {M}")
-    for name, t in (("data", w.data), ("scales", w.scales), ("gscales", w.gscales)):
+    data, scales, gs = w.data, w.scales, w.gscales
+    for name, t in (("data", data), ("scales", scales), ("gscales", gs)):
         if not isinstance(t, torch.Tensor) or t.device != dev:
             raise ValueError(f"w.{name} must be a tensor on {dev}")
-    if w.gscales.dtype != torch.float32 or not w.gscales.is_contiguous() or not w.scales.is_contiguous():
+    if gs.dtype is not torch.float32 or not gs.is_contiguous() or not scales.is_contiguous():
         raise TypeError("w.gscales must be contiguous float32, w.scales contiguous")
+    if data.element_size() != 1 or scales.element_size() != 1 or data.stride(-1) != 1:
+        raise TypeError("w.data and w.scales must be bytes, rows of w.data contiguous")
     # the device reads these without a check
     g = max(ng, 1)
     need = weight_rows * g
     if M and N and K:
-        _room("w.data", w.data, ((need - 1) * w.ld + K) // 2, "bytes are read")
-        _room("w.scales", w.scales, (need // 16 if int(w.block) == 2 else need) * (K // 16), "are read")
-        _room("w.gscales", w.gscales, g, "are read")
+        _room("w.data", data, ((need - 1) * w.ld + K) // 2)
+        _room("w.scales", scales, (need // 16 if w.block == Block.TILE else need) * (K // 16))
+        _room("w.gscales", gs, 4 * g)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     else:
         _check_tensor(out, "out", torch.bfloat16, 2, dev)
         if out.shape[0] < M or out.shape[1] < N or out.stride(1) != 1:
             raise ValueError(f"out must hold [{M}, {N}] with unit column stride")
-    _launch(dev, stream, fn, x.data_ptr(), x.stride(0), x.shape[0], ctypes.byref(w._c()), M, N, K, out.data_ptr(),
+    _launch(dev, fn, x.data_ptr(), x.stride(0), x.shape[0], ctypes.byref(w._c()), M, N, K, out.data_ptr(),
             out.stride(0), ng, _p(group_row_offsets), _p(x_row_index))
     return out
 
 
-def nvfp4_gemv(x, w, M, N, K, out=None, group_row_offsets=None, x_row_index=None, stream=None):
+@_takes_stream
+def nvfp4_gemv(x, w, M, N, K, out=None, group_row_offsets=None, x_row_index=None):
     """y[M, N] = x W^T for a few BF16 rows x and an NVFP4 weight Operand w
     [N, K] (as mx_gemm's b); x is used as it is, not quantized.  Grouped calls
     take int32 group_row_offsets [groups + 1] and one weight matrix per group;
     x_row_index [M] gathers rows of x."""
-    return _gemv(_lib().nvfp4_gemv, x, w, M, N, K, N, out, group_row_offsets, x_row_index, stream)
+    return _gemv(_lib().nvfp4_gemv, x, w, M, N, K, N, out, group_row_offsets, x_row_index)
 
 
-def nvfp4_gemv_swiglu(x, w, M, inter, K, out=None, group_row_offsets=None, x_row_index=None, stream=None):
+@_takes_stream
+def nvfp4_gemv_swiglu(x, w, M, inter, K, out=None, group_row_offsets=None, x_row_index=None):
     """h[M, inter] = silu(x Wg^T) * (x Wu^T) for a few BF16 rows x and an NVFP4
     gate_up Operand w (gate rows, then up rows, per group); arguments as
     nvfp4_gemv."""
-    return _gemv(_lib().nvfp4_gemv_swiglu, x, w, M, inter, K, 2 * inter, out, group_row_offsets, x_row_index, stream)
+    return _gemv(_lib().nvfp4_gemv_swiglu, x, w, M, inter, K, 2 * inter, out, group_row_offsets, x_row_index)
 
 
 # -------------------------------------------------------------------- the cache
@@ -177,6 +215,7 @@ class NVFP4Cache:
         stride = lambda t: t.stride(0) if pages > 1 else t[0].numel() if pages else 0
         self._c = _Cache(_p(k_codes), _p(k_scales), _p(k_gscales), _p(v_codes), _p(v_scales), _p(v_gscales), pages,
                          stride(k_codes), stride(k_scales), stride(k_gscales), heads, page, d)
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def empty(cls, num_pages, num_heads, page_size, head_dim, device="cuda"):
@@ -192,48 +231,55 @@ def _check_requests(cache, block_table, seq_lens, q_offsets, rows):
     if not isinstance(cache, NVFP4Cache):
         raise TypeError("cache must be an NVFP4Cache")
     dev = cache.device
-    _check_tensor(block_table, "block_table", torch.int32, 2, dev)
-    n = block_table.shape[0]
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+    if not _is(block_table, torch.int32, 2, dev):
+        _check_tensor(block_table, "block_table", torch.int32, 2, dev)
+    n, width = block_table.shape
+    if width > 1 and block_table.stride(1) != 1:
         raise ValueError("block_table must have unit column stride")
     _check_index(seq_lens, "seq_lens", n, dev)
     if q_offsets is not None:
         _check_index(q_offsets, "q_offsets", n + 1, dev)
     elif rows != n:
         raise ValueError(f"without q_offsets there is one row per request ({rows} rows, {n} requests)")
-    return dev
+    return dev, n, width, block_table.stride(0)
 
 
 def _check_rows(t, name, heads, d, rows, dev):
-    _check_tensor(t, name, torch.bfloat16, 3, dev)
-    if t.shape[2] != d or t.shape[0] != rows or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {tuple(t.shape)}")
-    if t.stride(2) != 1:
+    """[rows, heads, d] BF16 with unit stride along d (heads None: any); returns heads and the two strides."""
+    if not _is(t, torch.bfloat16, 3, dev):
+        _check_tensor(t, name, torch.bfloat16, 3, dev)
+    shape, (st, sh, sd) = t.shape, t.stride()
+    if shape[2] != d or shape[0] != rows or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {tuple(shape)}")
+    if sd != 1:
         raise ValueError(f"{name} must have unit stride along head_dim")
+    return shape[1], st, sh
 
 
-def nvfp4_cache_append(k, v, cache, block_table, seq_lens, q_offsets=None, with_dq=False, k_dq=None, v_dq=None,
-                       stream=None):
+@_takes_stream
+def nvfp4_cache_append(k, v, cache, block_table, seq_lens, q_offsets=None, with_dq=False, k_dq=None, v_dq=None):
     """Quantizes the BF16 rows k and v [tokens, heads, head_dim] into the cache.
     Request b has the rows q_offsets[b] .. q_offsets[b + 1] - 1 (one row each
     without q_offsets), its last tokens: seq_lens[b] counts them, and the pages
     come from block_table[b].  A row without a page is not stored.  With with_dq
     (or k_dq and v_dq) also returns the stored values in BF16, (k_dq, v_dq)."""
     T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0
-    dev = _check_requests(cache, block_table, seq_lens, q_offsets, T)
+    dev, n, width, ld = _check_requests(cache, block_table, seq_lens, q_offsets, T)
     h, d = cache.num_heads, cache.head_dim
-    _check_rows(k, "k", h, d, T, dev)
-    _check_rows(v, "v", h, d, T, dev)
+    _, kt, kh = _check_rows(k, "k", h, d, T, dev)
+    _, vt, vh = _check_rows(v, "v", h, d, T, dev)
     if with_dq or k_dq is not None or v_dq is not None:
-        k_dq = torch.empty((T, h, d), dtype=torch.bfloat16, device=dev) if k_dq is None else k_dq
-        v_dq = torch.empty((T, h, d), dtype=torch.bfloat16, device=dev) if v_dq is None else v_dq
-        for name, t in (("k_dq", k_dq), ("v_dq", v_dq)):
-            _check_rows(t, name, h, d, T, dev)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-    _launch(dev, stream, _lib().nvfp4_cache_append, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-            v.stride(1), T, ctypes.byref(cache._c), block_table.data_ptr(), block_table.stride(0),
-            block_table.shape[1], seq_lens.data_ptr(), _p(q_offsets), seq_lens.numel(), _p(k_dq), _p(v_dq))
+        if k_dq is None and v_dq is None:
+            k_dq, v_dq = torch.empty((2, T, h, d), dtype=torch.bfloat16, device=dev).unbind(0)
+        else:
+            k_dq = torch.empty((T, h, d), dtype=torch.bfloat16, device=dev) if k_dq is None else k_dq
+            v_dq = torch.empty((T, h, d), dtype=torch.bfloat16, device=dev) if v_dq is None else v_dq
+            for name, t in (("k_dq", k_dq), ("v_dq", v_dq)):
+                _check_rows(t, name, h, d, T, dev)
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+    _launch(dev, _lib().nvfp4_cache_append, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, T, cache._ref,
+            block_table.data_ptr(), ld, width, seq_lens.data_ptr(), _p(q_offsets), n, _p(k_dq), _p(v_dq))
     return (k_dq, v_dq) if k_dq is not None else None
 
 
@@ -243,8 +289,9 @@ def nvfp4_attention_workspace(tokens, q_heads, heads, head_dim, page_size, table
                                             bool(ragged))
 
 
+@_takes_stream
 def nvfp4_attention(q, cache, block_table, seq_lens, q_offsets=None, scale=None, window=0, out=None, with_lse=False,
-                    lse=None, workspace=None, stream=None):
+                    lse=None, workspace=None):
     """Causal attention of the BF16 query rows q [tokens, q_heads, head_dim]
     over the cache (requests as in nvfp4_cache_append; append their K and V
     first).  scale defaults to head_dim ** -0.5; window > 0 limits a row to
@@ -254,14 +301,14 @@ def nvfp4_attention(q, cache, block_table, seq_lens, q_offsets=None, scale=None,
     `workspace` is a uint8 tensor of nvfp4_attention_workspace() bytes, by
     default a fresh one."""
     T = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
-    dev = _check_requests(cache, block_table, seq_lens, q_offsets, T)
+    dev, n, width, ld = _check_requests(cache, block_table, seq_lens, q_offsets, T)
     d = cache.head_dim
-    _check_rows(q, "q", None, d, T, dev)
-    hq = q.shape[1]
+    hq, qt, qh = _check_rows(q, "q", None, d, T, dev)
     if out is None:
         out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
+        ot, oh = hq * d, d
     else:
-        _check_rows(out, "out", hq, d, T, dev)
+        _, ot, oh = _check_rows(out, "out", hq, d, T, dev)
     if lse is None and with_lse:
         lse = torch.empty((T, hq), dtype=torch.float32, device=dev)
     elif lse is not None:
@@ -269,7 +316,6 @@ def nvfp4_attention(q, cache, block_table, seq_lens, q_offsets=None, scale=None,
         if tuple(lse.shape) != (T, hq) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous [{T}, {hq}]")
     L = _lib()
-    n, width = block_table.shape
     need = L.nvfp4_attention_workspace(T, hq, cache.num_heads, d, cache.page_size, width, n, q_offsets is not None)
     have = 0
     if workspace is None:
@@ -279,8 +325,7 @@ def nvfp4_attention(q, cache, block_table, seq_lens, q_offsets=None, scale=None,
     else:
         _check_tensor(workspace, "workspace", torch.uint8, 1, dev)
         have = workspace.numel() if workspace.is_contiguous() else 0
-    _launch(dev, stream, L.nvfp4_attention, q.data_ptr(), q.stride(0), q.stride(1), T, hq, ctypes.byref(cache._c),
-            block_table.data_ptr(), block_table.stride(0), width, seq_lens.data_ptr(), _p(q_offsets), n,
-            d ** -0.5 if scale is None else scale, window, out.data_ptr(), out.stride(0), out.stride(1), _p(lse),
-            _p(workspace), have)
+    _launch(dev, L.nvfp4_attention, q.data_ptr(), qt, qh, T, hq, cache._ref, block_table.data_ptr(), ld, width,
+            seq_lens.data_ptr(), _p(q_offsets), n, d ** -0.5 if scale is None else scale, window, out.data_ptr(), ot, oh,
+            _p(lse), _p(workspace), have)
     return out if lse is None else (out, lse)
