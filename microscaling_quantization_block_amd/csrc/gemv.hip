@@ -24,6 +24,7 @@
 
 #include "mxq_device.h"
 #include "decode_kernels.h"
+#include "mxq_kernels.h"
 
 namespace mxq {
 
@@ -407,12 +408,178 @@ static hipError_t launch_dot_sl(const GemvArgs& a, bool one, hipStream_t st) {
   return one ? launch_dot_as<SL, SWI, 64, 1>(a, st) : launch_dot_as<SL, SWI, 64, MMX>(a, st);
 }
 
+// --------------------------------------------------------------- up to 16 rows
+//
+// The matrix instruction again, for K up to 4096: a wave keeps its one or two
+// chunks of x in registers (read once) and streams weight tiles past them, so
+// only the weights move.  They come by loads that write LDS themselves, whole
+// 128-byte lines of eight lanes each, AHEAD tiles in advance; no register
+// waits for them and no barrier is needed, since a wave reads only what it
+// loaded.  In LDS the 16-byte pieces of row c are exchanged by c / 2, so that
+// the 16 rows' pieces that the operand layout reads together lie in different
+// banks.  After each tile the waves' partial sums meet in LDS (two buffers, one
+// barrier per tile).
+
+constexpr int AHEAD = 4;                       // items in flight behind the one being multiplied
+constexpr int ITEM = 2048 + 256;               // LDS bytes: 16 rows of 256 codes, 16 rows of 16 scales
+
+__device__ __forceinline__ void gemv_load16(const void* p, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void gemv_load4(const void* p, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+
+template <int SL, bool SWI, int XC>
+__global__ __launch_bounds__(512, 2) void gemv_stream_kernel(GemvArgs a, int tiles_per_wg) {
+  constexpr int R = SWI ? 2 : 1, PER = R * XC; // items of a tile: weight tiles times chunks
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_gemv[];   // [waves][AHEAD + 1] items, then the partial sums
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
+  const int c = lane & 15, g = lane >> 4;
+  const int grp = blockIdx.y;
+  int64_t m_begin = 0, m_end = a.M;
+  if (a.num_groups) {
+    m_begin = a.offsets[grp];
+    m_end = a.offsets[grp + 1];
+    m_begin = m_begin < 0 ? 0 : m_begin;
+    m_end = m_end > a.M ? a.M : m_end;
+  }
+  if (m_begin >= m_end) return;
+  const int64_t B = a.K >> 4;
+  const int tiles = (int)((a.N + 15) >> 4), t0 = blockIdx.x * tiles_per_wg, t1 = min(t0 + tiles_per_wg, tiles);
+  if (t0 >= t1) return;
+  const int chunks = (int)((a.K + 255) >> 8);
+  const float S = a.gs[grp];
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(s_gemv) + wave * (AHEAD + 1) * ITEM;
+  const uint8_t* ring = s_gemv + wave * (AHEAD + 1) * ITEM;
+  float* red = reinterpret_cast<float*>(s_gemv + nw * (AHEAD + 1) * ITEM);   // [2][waves][R][16 m][16 n]
+
+  // what a lane loads of an item: of rows lane / 8 and 8 + lane / 8 the 16-byte piece that belongs at
+  // place lane % 8, and of row lane / 4 the four scales lane % 4
+  const uint8_t* wbase = a.w + grp * a.w_group;
+  const uint8_t* sbase = a.scales + grp * a.s_group;
+  auto issue = [&](int item, int slot) {       // item = (tile - t0) * PER + r * XC + x; behind the last: some item again
+    const int tile = min(t0 + item / PER, t1 - 1), r = item % PER / XC, x = item % XC;
+    const int ch = min(wave + x * nw, chunks - 1);
+    const int64_t k0 = (int64_t)ch * 256;
+    const int left = (int)(a.K - k0 < 256 ? a.K - k0 : 256);   // a multiple of 64
+    const uint32_t lds = lds0 + slot * ITEM;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");         // the slot's last readers have their values
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int lr = 8 * h + (lane >> 3);
+      int piece = (lane & 7) ^ (lr >> 1);
+      piece = 32 * piece < left ? piece : 0;   // behind K: any codes, x is zero there
+      int64_t row = (int64_t)tile * 16 + lr;
+      row = (row < a.N ? row : a.N - 1) + (SWI && r ? a.N : 0);
+      gemv_load16(wbase + row * a.ld_w + (k0 >> 1) + 16 * piece, lds + 1024 * h);
+    }
+    const int word = 64 * (lane & 3) < left ? lane & 3 : 0;
+    int64_t row = (int64_t)tile * 16 + (lane >> 2);
+    row = (row < a.N ? row : a.N - 1) + (SWI && r ? a.N : 0);
+    gemv_load4(sbase + gemv_scale_offset<SL>(row, (k0 >> 4) + 4 * word, B), lds + 2048);
+  };
+
+  for (int64_t m0 = m_begin; m0 < m_end; m0 += 16) {
+    // x: lane (c, g) holds row m0 + c, the values 64 g + 8 j of its chunks; zero where there is none
+    uint4 x[XC][8];
+    {
+      const int64_t m = m0 + c;
+      int64_t xr = m;
+      bool have = m < m_end;
+      if (have && a.row_index) xr = a.row_index[m];
+      have = have && xr >= 0 && xr < a.x_rows;
+#pragma unroll
+      for (int q = 0; q < XC; ++q) {
+        const int64_t k = (int64_t)(wave + q * nw) * 256 + 64 * g;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[q][j] = make_uint4(0, 0, 0, 0);
+        if (have && k < a.K)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[q][j] = *reinterpret_cast<const uint4*>(a.x + xr * a.ld_x + k + 8 * j);
+      }
+    }
+    const int cols = (int)(m_end - m0 < 16 ? m_end - m0 : 16);
+    // nothing of the compiler's is in flight from here on but stores of y, which a wait may take for loads
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (int i = 0; i < AHEAD; ++i) issue(i, i);
+    int item = 0, slot = 0;
+    for (int t = t0; t < t1; ++t) {
+      f32x4 acc[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const int r = q / XC, xi = q % XC;
+        issue(item + AHEAD, slot ? slot - 1 : AHEAD);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"i"(3 * AHEAD) : "memory");
+        const uint8_t* it = ring + slot * ITEM;
+        const uint4 w0 = *reinterpret_cast<const uint4*>(it + c * 128 + (((2 * g) ^ (c >> 1)) << 4));
+        const uint4 w1 = *reinterpret_cast<const uint4*>(it + c * 128 + (((2 * g + 1) ^ (c >> 1)) << 4));
+        const uint32_t s = *reinterpret_cast<const uint32_t*>(it + 2048 + 16 * c + 4 * g);
+        const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bf16x8 av = e2m1x8_to_bf16(ww[j], e4m3_to_f32((s >> (8 * (j >> 1))) & 0xFF));
+          acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8, x[xi][j]), acc[r], 0, 0, 0);
+        }
+        ++item;
+        slot = slot == AHEAD ? 0 : slot + 1;
+      }
+      float* buf = red + (t & 1) * nw * R * 256;
+#pragma unroll
+      for (int r = 0; r < R; ++r) *reinterpret_cast<f32x4*>(&buf[((wave * R + r) * 16 + c) * 16 + 4 * g]) = acc[r];
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      for (int i = threadIdx.x; i < cols * 16; i += blockDim.x) {
+        const int n = i & 15, m = i >> 4;
+        float v[2];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          v[r] = 0.0f;
+          for (int w = 0; w < nw; ++w) v[r] += buf[((w * R + r) * 16 + m) * 16 + n];
+          v[r] *= S;
+        }
+        const float out = SWI ? v[0] / (1.0f + expf(-v[0])) * v[R - 1] : v[0];
+        const int64_t col = (int64_t)t * 16 + n;
+        if (col < a.N) a.y[(m0 + m) * a.ld_y + col] = (uint16_t)f32x2_to_bf16x2(out, 0.0f);
+      }
+    }
+    // the loads behind the last item must not write LDS after this
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+}
+
+template <int SL, bool SWI, int XC>
+static hipError_t launch_stream_as(const GemvArgs& a, int nw, hipStream_t st) {
+  const int lds = nw * (AHEAD + 1) * ITEM + 2 * nw * (SWI ? 2 : 1) * 1024;
+  static std::atomic<uint32_t> done{0};
+  hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&gemv_stream_kernel<SL, SWI, XC>), 160 * 1024, done);
+  if (e != hipSuccess) return e;
+  const int64_t groups = a.num_groups ? a.num_groups : 1, tiles = (a.N + 15) / 16;
+  // as many workgroups as the chip holds at once, twice that for groups, of which some are empty
+  const int64_t resident = 256 * (160 * 1024 / lds), want = a.num_groups ? 2 * resident : resident;
+  const int64_t wgs = want / groups < 1 ? 1 : want / groups > tiles ? tiles : want / groups;
+  const int64_t per = (tiles + wgs - 1) / wgs;
+  const dim3 grid((unsigned)((tiles + per - 1) / per), (unsigned)groups);
+  hipLaunchKernelGGL((gemv_stream_kernel<SL, SWI, XC>), grid, dim3(64 * nw), lds, st, a, (int)per);
+  return hipGetLastError();
+}
+
+// Whole words and pieces: what its loads need.
+static bool can_stream(const GemvArgs& a) {
+  return a.K % 64 == 0 && a.K <= 4096 && a.ld_w % 16 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0;
+}
+
 template <int SL, bool SWI>
 static hipError_t launch_gemv_sl(const GemvArgs& a, hipStream_t st) {
   const int64_t groups = a.num_groups ? a.num_groups : 1;
   const int64_t rows = (a.M + groups - 1) / groups;            // of x, per matrix
   const int64_t tiles = (a.N + 15) / 16 * groups;
   if (rows <= 3 && a.K >= 32 && a.K <= 16384) return launch_dot_sl<SL, SWI>(a, rows == 1, st);
+  if (rows <= 16 && can_stream(a)) {
+    const int chunks = (int)((a.K + 255) >> 8);
+    return chunks <= 8 ? launch_stream_as<SL, SWI, 1>(a, chunks, st) : launch_stream_as<SL, SWI, 2>(a, (chunks + 1) / 2, st);
+  }
   if (rows > 16) return launch_gemv_as<SL, SWI, 2, 2>(a, st);
   if (tiles >= 2048) return launch_gemv_as<SL, SWI, 4, 1>(a, st);
   if (SWI || tiles >= 1024) return launch_gemv_as<SL, SWI, 2, 1>(a, st);
