@@ -413,14 +413,13 @@ static hipError_t launch_dot_sl(const GemvArgs& a, bool one, hipStream_t st) {
 // The matrix instruction again, for K up to 4096: a wave keeps its one or two
 // chunks of x in registers (read once) and streams weight tiles past them, so
 // only the weights move.  They come by loads that write LDS themselves, whole
-// 128-byte lines of eight lanes each, AHEAD tiles in advance; no register
+// 128-byte lines of eight lanes each, AHEAD items in advance; no register
 // waits for them and no barrier is needed, since a wave reads only what it
 // loaded.  In LDS the 16-byte pieces of row c are exchanged by c / 2, so that
 // the 16 rows' pieces that the operand layout reads together lie in different
 // banks.  After each tile the waves' partial sums meet in LDS (two buffers, one
 // barrier per tile).
 
-constexpr int AHEAD = 4;                       // items in flight behind the one being multiplied
 constexpr int ITEM = 2048 + 256;               // LDS bytes: 16 rows of 256 codes, 16 rows of 16 scales
 
 __device__ __forceinline__ void gemv_load16(const void* p, uint32_t lds) {
@@ -430,7 +429,11 @@ __device__ __forceinline__ void gemv_load4(const void* p, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
 }
 
-template <int SL, bool SWI, int XC>
+// AHEAD: items in flight behind the one being multiplied.  Three for eight
+// waves (13 rows through 24576 x 4096: 21.1 us, four 21.5, two 25.9); two where
+// a few waves are enough for K, for more workgroups on a compute unit (64 tokens
+// through 128 experts, 2048 x 768: 32.5 us, three 35.6, four 37.7).
+template <int SL, bool SWI, int XC, int AHEAD>
 __global__ __launch_bounds__(512, 2) void gemv_stream_kernel(GemvArgs a, int tiles_per_wg) {
   constexpr int R = SWI ? 2 : 1, PER = R * XC; // items of a tile: weight tiles times chunks
   extern __shared__ __attribute__((aligned(16))) uint8_t s_gemv[];   // [waves][AHEAD + 1] items, then the partial sums
@@ -549,11 +552,11 @@ __global__ __launch_bounds__(512, 2) void gemv_stream_kernel(GemvArgs a, int til
   }
 }
 
-template <int SL, bool SWI, int XC>
+template <int SL, bool SWI, int XC, int AHEAD>
 static hipError_t launch_stream_as(const GemvArgs& a, int nw, hipStream_t st) {
   const int lds = nw * (AHEAD + 1) * ITEM + 2 * nw * (SWI ? 2 : 1) * 1024;
   static std::atomic<uint32_t> done{0};
-  hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&gemv_stream_kernel<SL, SWI, XC>), 160 * 1024, done);
+  hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&gemv_stream_kernel<SL, SWI, XC, AHEAD>), 160 * 1024, done);
   if (e != hipSuccess) return e;
   const int64_t groups = a.num_groups ? a.num_groups : 1, tiles = (a.N + 15) / 16;
   // as many workgroups as the chip holds at once, twice that for groups, of which some are empty
@@ -561,7 +564,7 @@ static hipError_t launch_stream_as(const GemvArgs& a, int nw, hipStream_t st) {
   const int64_t wgs = want / groups < 1 ? 1 : want / groups > tiles ? tiles : want / groups;
   const int64_t per = (tiles + wgs - 1) / wgs;
   const dim3 grid((unsigned)((tiles + per - 1) / per), (unsigned)groups);
-  hipLaunchKernelGGL((gemv_stream_kernel<SL, SWI, XC>), grid, dim3(64 * nw), lds, st, a, (int)per);
+  hipLaunchKernelGGL((gemv_stream_kernel<SL, SWI, XC, AHEAD>), grid, dim3(64 * nw), lds, st, a, (int)per);
   return hipGetLastError();
 }
 
@@ -578,7 +581,8 @@ static hipError_t launch_gemv_sl(const GemvArgs& a, hipStream_t st) {
   if (rows <= 3 && a.K >= 32 && a.K <= 16384) return launch_dot_sl<SL, SWI>(a, rows == 1, st);
   if (rows <= 16 && can_stream(a)) {
     const int chunks = (int)((a.K + 255) >> 8);
-    return chunks <= 8 ? launch_stream_as<SL, SWI, 1>(a, chunks, st) : launch_stream_as<SL, SWI, 2>(a, (chunks + 1) / 2, st);
+    if (chunks > 8) return launch_stream_as<SL, SWI, 2, 3>(a, (chunks + 1) / 2, st);
+    return chunks > 4 ? launch_stream_as<SL, SWI, 1, 3>(a, chunks, st) : launch_stream_as<SL, SWI, 1, 2>(a, chunks, st);
   }
   if (rows > 16) return launch_gemv_as<SL, SWI, 2, 2>(a, st);
   if (tiles >= 2048) return launch_gemv_as<SL, SWI, 4, 1>(a, st);
