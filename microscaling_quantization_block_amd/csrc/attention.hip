@@ -55,9 +55,8 @@ __device__ __forceinline__ f16x2 e4m3_pair(uint32_t w) {
   return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI);
 }
 
-// What a wave reads of one 32-token tile: whole words (a narrower load is
-// widened by the compiler as soon as it is issued, which waits for it), from
-// which the lane shifts its share.
+// What a lane takes of one 32-token tile: whole words, from which it shifts
+// its share.
 template <int D>
 struct RawTile {
   uint32_t k[2][D / 32];        // [half][dword]: token c of the half, values g D / 4 + 8 j ..
@@ -72,34 +71,6 @@ template <int D>
 __device__ __forceinline__ int ks_shift(int g) { return D == 64 ? 8 * g : D == 128 ? 16 * (g & 1) : 0; }
 template <int D>
 __device__ __forceinline__ int v_shift(int c) { return D == 64 ? 16 * (c & 1) : 0; }
-
-// Loads through a buffer descriptor: a uniform base, a uniform and a lane's
-// 32-bit offset, so a load needs no address registers of its own.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, -1, 0x00020000);
-}
-__device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t uniform) {
-  return __builtin_amdgcn_raw_buffer_load_b32(b, lane, uniform, 0);
-}
-__device__ __forceinline__ uint2 load2(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t uniform) {
-  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(b, lane, uniform, 0));
-}
-__device__ __forceinline__ uint4 load4(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t uniform) {
-  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(b, lane, uniform, 0));
-}
-
-// A lane's offsets inside a 16-token half of a page.
-template <int D>
-struct LaneOffsets {
-  uint32_t k, ks, v, vs, g;
-  __device__ __forceinline__ LaneOffsets(const CacheArgs& cc, int c, int g_) {
-    k = c * (D / 2) + g_ * (D / 8);
-    ks = c * (D / 16) + (g_ * (D / 64) & ~3);
-    v = 4 * g_ * (D / 2) + (c * (D / 32) & ~3);
-    vs = ((c * (D / 16) / 16) << cc.P_log2) + 4 * g_;
-    g = 16 * g_;
-  }
-};
 
 // The pages of a tile's halves (16 tokens lie in one page), -1 for none.
 struct TilePages {
@@ -120,45 +91,6 @@ __device__ __forceinline__ TilePages tile_pages(const CacheArgs& cc, ScalarTable
     r.p[s] = p < (int)cc.pages ? p : -1;
   }
   return r;
-}
-
-// Issues the loads of a tile.  A half without a page reads page 0.
-template <int D>
-__device__ __forceinline__ void load_tile(const CacheArgs& cc, const TilePages& tp, int h, int tile,
-                                          const LaneOffsets<D>& o, RawTile<D>& r) {
-  const int P = 1 << cc.P_log2;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int64_t page = tp.p[s] < 0 ? 0 : tp.p[s];
-    const uint32_t slot = (tile * TILE + 16 * s) & (P - 1);
-    const int64_t head = (int64_t)h * P;
-    const auto kc = buffer_at(cc.kc + page * cc.pc + head * (D / 2)), vc = buffer_at(cc.vc + page * cc.pc + head * (D / 2));
-    const auto ks = buffer_at(cc.ks + page * cc.psc + head * (D / 16)), vs = buffer_at(cc.vs + page * cc.psc + head * (D / 16));
-    const auto kg = buffer_at(cc.kg + page * cc.pg + head), vg = buffer_at(cc.vg + page * cc.pg + head);
-    if (D == 64) {
-      const uint2 w = load2(kc, o.k, slot * (D / 2));
-      r.k[s][0] = w.x, r.k[s][1] = w.y;
-    } else {
-#pragma unroll
-      for (int j = 0; j < D / 128; ++j) {
-        const uint4 w = load4(kc, o.k + 16 * j, slot * (D / 2));
-        r.k[s][4 * j] = w.x, r.k[s][4 * j + 1] = w.y, r.k[s][4 * j + 2] = w.z, r.k[s][4 * j + 3] = w.w;
-      }
-    }
-    r.ks[s] = load1(ks, o.ks, slot * (D / 16));
-    r.kg[s] = __builtin_bit_cast(f32x4, load4(kg, o.g, slot * 4));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (D == 256) {
-        const uint2 w = load2(vc, o.v + i * (D / 2), slot * (D / 2));
-        r.v[s][i][0] = w.x, r.v[s][i][(D + 127) / 128 - 1] = w.y;
-      } else {
-        r.v[s][i][0] = load1(vc, o.v + i * (D / 2), slot * (D / 2));
-      }
-    }
-    r.vs[s] = load1(vs, o.vs, slot);
-    r.vg[s] = __builtin_bit_cast(f32x4, load4(vg, o.g, slot * 4));
-  }
 }
 
 // max without the quieting of signalling NaNs that fmaxf adds to values whose
@@ -474,11 +406,127 @@ __device__ __forceinline__ void store_index(const AttnArgs& a, const Unit& u, in
     a.part_index[u.b] = make_int2((int)u.base, u.chunks);
 }
 
+// ------------------------------------------------------- raw tiles through LDS
+//
+// A 32-token tile in LDS, as it is stored: codes [32, D / 2] of K, of V, scales
+// [32, D / 16] of K, [D / 16, 32] of V, second scales of K, of V.  It is loaded by
+// instructions that write LDS themselves, 1 KiB of codes or 64 words of scales
+// each: neighbouring lanes read neighbouring bytes (as the operands of the
+// matrix instruction lie in registers they would not), and no register waits.
+template <int D>
+struct RawLayout {
+  static constexpr int CODES = 16 * D, KS = 2 * CODES, VS = KS + 2 * D, KG = VS + 2 * D, VG = KG + 128, SIZE = VG + 128;
+  static constexpr int CODE_JOBS = 2 * D / 64, JOBS = CODE_JOBS + (D + 64) / 64;
+};
+// LDS row of V's row r: four neighbouring rows are rotated by r / 4, so that the
+// lane groups, which read rows four apart, meet different banks.
+__device__ __forceinline__ int v_row(int r) { return (r & ~3) | ((r + (r >> 2)) & 3); }
+// Place of K's 16-byte piece q of row r, exchanged inside the row so that the
+// same piece of 16 rows lies in different banks.
+template <int D>
+__device__ __forceinline__ int k_piece(int r, int q) { return q ^ ((r / (512 / D)) & (D / 32 - 1)); }
+
+// A wave's part in loading the tiles: per lane a base address, and what a page
+// and a token in it add to that.
+struct TileLoad {
+  const uint8_t* base;
+  uint32_t page_stride, slot_stride;
+  int half;                     // of the tile
+  uint32_t lds;                 // uniform, inside the raw tile
+};
+template <int D>
+__device__ __forceinline__ TileLoad tile_load(const CacheArgs& cc, int h, int job, int lane) {
+  using Y = RawLayout<D>;
+  const int64_t P = 1 << cc.P_log2;
+  TileLoad t;
+  if (job < Y::CODE_JOBS) {
+    const bool v = job >= Y::CODE_JOBS / 2;
+    const int q = v ? job - Y::CODE_JOBS / 2 : job;
+    const int i = 64 * q + lane, at = i / (D / 32), chunk = i % (D / 32);
+    const int r = v ? (at & ~3) | ((at - (at >> 2)) & 3) : at;  // the row that belongs there
+    t.base = (v ? cc.vc : cc.kc) + (h * P + (r & 15)) * (D / 2) + 16 * (v ? chunk : k_piece<D>(r, chunk));
+    t.page_stride = (uint32_t)cc.pc;
+    t.slot_stride = D / 2;
+    t.half = r >> 4;
+    t.lds = (v ? Y::CODES : 0) + 1024 * q;
+    return t;
+  }
+  const int q = job - Y::CODE_JOBS, w = 64 * q + lane;          // word w of the scales
+  t.lds = Y::KS + 256 * q;
+  t.page_stride = (uint32_t)cc.psc;
+  if (w < D / 2) {
+    const int r = w / (D / 64);
+    t.base = cc.ks + (h * P + (r & 15)) * (D / 16) + 4 * (w % (D / 64));
+    t.slot_stride = D / 16;
+    t.half = r >> 4;
+  } else if (w < D) {
+    const int i = w - D / 2;
+    t.base = cc.vs + ((int64_t)h * (D / 16) + (i >> 3)) * P + 4 * (i & 3);
+    t.slot_stride = 1;
+    t.half = (i >> 2) & 1;
+  } else {
+    const int i = w - D, r = i & 31;
+    t.base = reinterpret_cast<const uint8_t*>((i < 32 ? cc.kg : cc.vg) + h * P + (r & 15));
+    t.page_stride = (uint32_t)(4 * cc.pg);
+    t.slot_stride = 4;
+    t.half = r >> 4;
+  }
+  return t;
+}
+// Loads that write LDS at m0 + lane * size; no register receives them.
+__device__ __forceinline__ void load_lds16(const void* p, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void load_lds4(const void* p, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
 // ------------------------------------------------------------- a few columns
 //
 // The four waves of a workgroup hold the same 16 NQ columns and take every
 // fourth tile of the chunk each; they are joined in LDS.  Nothing is shared in
-// between, so a wave dequantizes what it multiplies.
+// between, so a wave dequantizes what it multiplies, and a ring of raw tiles of
+// its own, FEW_AHEAD of them in flight, needs no barrier.
+constexpr int FEW_AHEAD = 1;
+template <int D, int NQ>
+constexpr int few_lds() {
+  const int ring = FEW_WAVES * (FEW_AHEAD + 1) * RawLayout<D>::SIZE;
+  const int join = ((FEW_WAVES - 1) * 16 * NQ * D + FEW_WAVES * 16 * NQ * 2) * 4;
+  return ring > join ? ring : join;
+}
+
+// A lane's part of a raw tile in LDS.
+template <int D>
+__device__ __forceinline__ void read_tile(const uint8_t* raw, int c, int g, RawTile<D>& r) {
+  using Y = RawLayout<D>;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int row = 16 * s + c;
+    if (D == 64) {
+      const uint2 w = *reinterpret_cast<const uint2*>(raw + row * 32 + 16 * k_piece<D>(row, g >> 1) + 8 * (g & 1));
+      r.k[s][0] = w.x, r.k[s][1] = w.y;
+    } else {
+#pragma unroll
+      for (int j = 0; j < D / 128; ++j) {
+        const uint4 w = *reinterpret_cast<const uint4*>(raw + row * (D / 2) + 16 * k_piece<D>(row, g * (D / 128) + j));
+        r.k[s][4 * j] = w.x, r.k[s][4 * j + 1] = w.y, r.k[s][4 * j + 2] = w.z, r.k[s][4 * j + 3] = w.w;
+      }
+    }
+    r.ks[s] = *reinterpret_cast<const uint32_t*>(raw + Y::KS + row * (D / 16) + (g * (D / 64) & ~3));
+    r.kg[s] = *reinterpret_cast<const f32x4*>(raw + Y::KG + 4 * (16 * s + 4 * g));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* v = raw + Y::CODES + v_row(16 * s + 4 * g + i) * (D / 2) + (c * (D / 32) & ~3);
+      if (D == 256) {
+        const uint2 w = *reinterpret_cast<const uint2*>(v);
+        r.v[s][i][0] = w.x, r.v[s][i][(D + 127) / 128 - 1] = w.y;
+      } else {
+        r.v[s][i][0] = *reinterpret_cast<const uint32_t*>(v);
+      }
+    }
+    r.vs[s] = *reinterpret_cast<const uint32_t*>(raw + Y::VS + (c * (D / 16) / 16) * 32 + 16 * s + 4 * g);
+    r.vg[s] = *reinterpret_cast<const f32x4*>(raw + Y::VG + 4 * (16 * s + 4 * g));
+  }
+}
 
 // One tile.  `inside`: every token is in reach of every column.
 template <int D, int NQ>
@@ -588,9 +636,11 @@ __device__ __forceinline__ void attend_tile(Columns<D, NQ>& o, float* l, RawTile
 
 template <int D, int NQ>
 __global__ __launch_bounds__(256, D <= 128 && NQ == 1 ? 3 : 2) void attention_few_kernel(AttnArgs a) {
-  constexpr int ND = D / 16, CT = 16 * NQ;
-  __shared__ float s_o[(FEW_WAVES - 1) * CT * D];
-  __shared__ float s_ml[FEW_WAVES * CT * 2];
+  using Y = RawLayout<D>;
+  constexpr int ND = D / 16, CT = 16 * NQ, SLOTS = FEW_AHEAD + 1;
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_few[];   // [waves][SLOTS] raw tiles; then the join
+  float* s_ml = reinterpret_cast<float*>(s_few);
+  float* s_o = s_ml + FEW_WAVES * CT * 2;
   const CacheArgs& cc = a.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -606,35 +656,56 @@ __global__ __launch_bounds__(256, D <= 128 && NQ == 1 ? 3 : 2) void attention_fe
   const int2 tiles = chunk_tiles(u, re);
   float l[NQ] = {};
 
-  // a tile's loads are in flight while the one before it is computed, and the
-  // page numbers of the next but one
-  int tile = tiles.x + wave;
-  if (tile < tiles.y) {
-    const LaneOffsets<D> off(cc, c, g);
-    RawTile<D> r[2];
-    TilePages tp[2];
-    tp[0] = tile_pages(cc, table, tile);
-    tp[1] = tile_pages(cc, table, tile + FEW_WAVES);
-    load_tile<D>(cc, tp[0], h, tile, off, r[0]);
-    while (true) {
+  if (tiles.x + wave < tiles.y) {
+    TileLoad job[Y::JOBS];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        // unconditional, so that the waits count them: behind the last tile
-        // they read page 0, which stays unused
-        const bool more = tile + FEW_WAVES < tiles.y;
-        if (!more) tp[1 - k].p[0] = tp[1 - k].p[1] = -1;
-        load_tile<D>(cc, tp[1 - k], h, tile + FEW_WAVES, off, r[1 - k]);
-        const TilePages now = tp[k];
-        tp[k] = tile_pages(cc, table, tile + 2 * FEW_WAVES);
-        const bool inside =
-            tile * TILE >= re.all_begin && (tile + 1) * TILE <= re.all_end && now.p[0] >= 0 && now.p[1] >= 0;
-        attend_tile<D, NQ>(o, l, r[k], now, tile, re.begin, re.end, inside, c, g);
-        if (!more) goto done;
-        tile += FEW_WAVES;
+    for (int k = 0; k < Y::JOBS; ++k) job[k] = tile_load<D>(cc, h, k, lane);
+    const uint8_t* ring = s_few + wave * SLOTS * Y::SIZE;
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(ring);
+    const int page_mask = (1 << cc.P_log2) - 1;
+    uint32_t ok = 0;                           // halves with a page: two bits per tile in flight, the current lowest
+    int ahead = tiles.x + wave;                // the tile to be issued next, and its pages
+    TilePages pages = tile_pages(cc, table, ahead);
+    // behind the last tile the loads read page 0, which stays unused, so that
+    // the number in flight is always the same
+    auto issue = [&](int slot, int behind) {
+      TilePages tp = pages;
+      if (ahead >= tiles.y) tp.p[0] = tp.p[1] = -1;
+      ok |= (uint32_t)((tp.p[0] >= 0) | (tp.p[1] >= 0) << 1) << (2 * behind);
+      const int p0 = max(tp.p[0], 0), p1 = max(tp.p[1], 0);
+      const int s0 = (ahead * TILE) & page_mask, s1 = (ahead * TILE + 16) & page_mask;
+      const uint32_t raw = lds0 + slot * Y::SIZE;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");        // the slot's last readers have their values
+#pragma unroll
+      for (int k = 0; k < Y::JOBS; ++k) {
+        const TileLoad& t = job[k];
+        const uint8_t* p8 = t.base + (uint64_t)(uint32_t)(t.half ? p1 : p0) * t.page_stride +
+                            (uint32_t)(t.half ? s1 : s0) * t.slot_stride;
+        if (k < Y::CODE_JOBS) load_lds16(p8, raw + t.lds);
+        else load_lds4(p8, raw + t.lds);
       }
+      ahead += FEW_WAVES;
+      pages = tile_pages(cc, table, ahead);
+    };
+#pragma unroll
+    for (int i = 0; i < FEW_AHEAD; ++i) issue(i, i);
+    int slot = 0;
+    for (int tile = tiles.x + wave; tile < tiles.y; tile += FEW_WAVES) {
+      issue(slot ? slot - 1 : FEW_AHEAD, FEW_AHEAD);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"i"(FEW_AHEAD * Y::JOBS) : "memory");
+      RawTile<D> r;
+      read_tile<D>(ring + slot * Y::SIZE, c, g, r);
+      TilePages now;
+      now.p[0] = ok & 1 ? 0 : -1;
+      now.p[1] = ok & 2 ? 0 : -1;
+      const bool inside = (tile * TILE >= re.all_begin) & ((tile + 1) * TILE <= re.all_end) & ((ok & 3) == 3);
+      attend_tile<D, NQ>(o, l, r, now, tile, re.begin, re.end, inside, c, g);
+      ok >>= 2;
+      slot = slot == FEW_AHEAD ? 0 : slot + 1;
     }
   }
-done:
+  // the loads behind the last tile have landed in every wave's ring before it is used again
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   // join the four waves' tokens: the common maximum and sum first, then the
   // rows, each wave's brought to the common scale before it enters LDS
@@ -723,70 +794,11 @@ struct ManyLayout {
   static constexpr int W = MANY_WAVES, CT = 32 * W;
   static constexpr int PH = D <= 128 ? 2 : 1, RING = 4;         // tiles of a phase, phases of raw tiles
   static constexpr int NK = D / 16, NV = D / 16, F = NK + NV;   // fragments of a tile
-  // a raw tile: codes [32, D / 2] of K, of V, scales [32, D / 16] of K, [D / 16, 32] of V, second scales
-  static constexpr int CODES = 16 * D, KS = 2 * CODES, VS = KS + 2 * D, KG = VS + 2 * D, VG = KG + 128, RAW = VG + 128;
+  using Raw = RawLayout<D>;
+  static constexpr int CODES = Raw::CODES, KS = Raw::KS, VS = Raw::VS, KG = Raw::KG, VG = Raw::VG, RAW = Raw::SIZE;
   static constexpr int RAW0 = 2 * PH * F * 1024, LDS = RAW0 + RING * PH * RAW;
-  // load instructions of a tile: 1 KiB of codes each, or 64 words of scales
-  static constexpr int CODE_JOBS = 2 * D / 64, JOBS = CODE_JOBS + (D + 64) / 64, JW = (JOBS + W - 1) / W;
+  static constexpr int CODE_JOBS = Raw::CODE_JOBS, JOBS = Raw::JOBS, JW = (JOBS + W - 1) / W;   // JW: of a wave
 };
-// LDS row of V's row r: four neighbouring rows are rotated by r / 4, so that the
-// two lane halves, which read rows four apart, meet different banks.
-__device__ __forceinline__ int v_row(int r) { return (r & ~3) | ((r + (r >> 2)) & 3); }
-
-// A wave's part in loading the tiles: per lane a base address, and what a page
-// and a token in it add to that.
-struct TileLoad {
-  const uint8_t* base;
-  uint32_t page_stride, slot_stride;
-  int half;                     // of the tile
-  uint32_t lds;                 // uniform, inside the raw tile
-};
-template <int D>
-__device__ __forceinline__ TileLoad tile_load(const CacheArgs& cc, int h, int job, int lane) {
-  using Y = ManyLayout<D>;
-  const int64_t P = 1 << cc.P_log2;
-  TileLoad t;
-  if (job < Y::CODE_JOBS) {
-    const bool v = job >= Y::CODE_JOBS / 2;
-    const int q = v ? job - Y::CODE_JOBS / 2 : job;
-    const int i = 64 * q + lane, at = i / (D / 32), chunk = i % (D / 32);
-    const int r = v ? (at & ~3) | ((at - (at >> 2)) & 3) : at;  // the row that belongs there
-    t.base = (v ? cc.vc : cc.kc) + (h * P + (r & 15)) * (D / 2) + 16 * chunk;
-    t.page_stride = (uint32_t)cc.pc;
-    t.slot_stride = D / 2;
-    t.half = r >> 4;
-    t.lds = (v ? Y::CODES : 0) + 1024 * q;
-    return t;
-  }
-  const int q = job - Y::CODE_JOBS, w = 64 * q + lane;          // word w of the scales
-  t.lds = Y::KS + 256 * q;
-  t.page_stride = (uint32_t)cc.psc;
-  if (w < D / 2) {
-    const int r = w / (D / 64);
-    t.base = cc.ks + (h * P + (r & 15)) * (D / 16) + 4 * (w % (D / 64));
-    t.slot_stride = D / 16;
-    t.half = r >> 4;
-  } else if (w < D) {
-    const int i = w - D / 2;
-    t.base = cc.vs + ((int64_t)h * (D / 16) + (i >> 3)) * P + 4 * (i & 3);
-    t.slot_stride = 1;
-    t.half = (i >> 2) & 1;
-  } else {
-    const int i = w - D, r = i & 31;
-    t.base = reinterpret_cast<const uint8_t*>((i < 32 ? cc.kg : cc.vg) + h * P + (r & 15));
-    t.page_stride = (uint32_t)(4 * cc.pg);
-    t.slot_stride = 4;
-    t.half = r >> 4;
-  }
-  return t;
-}
-// Loads that write LDS at m0 + lane * size; no register receives them.
-__device__ __forceinline__ void load_lds16(const void* p, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds) : "memory");
-}
-__device__ __forceinline__ void load_lds4(const void* p, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
-}
 // Waits until at most N of the wave's loads are in flight and for its LDS
 // accesses, then for the workgroup.
 template <int N>
@@ -915,7 +927,8 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
 #pragma unroll
       for (int k = 0; k < (NK + W - 1) / W; ++k) {
         const int j = kfirst + W * k, word = hh * NK + j;       // of the token's codes
-        const uint32_t code = *reinterpret_cast<const uint32_t*>(raw + c * (D / 2) + 4 * word);
+        const uint32_t code =
+            *reinterpret_cast<const uint32_t*>(raw + c * (D / 2) + 16 * k_piece<D>(c, word >> 2) + 4 * (word & 3));
         const uint32_t sc = raw[Y::KS + c * (D / 16) + (word >> 1)];
         frag[64 * j] = __builtin_bit_cast(uint4, k_fragment(code, e4m3_pair<false>(sc).x));
       }
@@ -1142,6 +1155,15 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int CT)
     a.lse[row] = total > 0.0f ? (mx + __builtin_amdgcn_logf(total)) * 0.693147180559945309f : NEG_INF;
 }
 
+template <int D, int NQ>
+static hipError_t launch_few(const AttnArgs& a, dim3 grid, hipStream_t st) {
+  static std::atomic<uint32_t> done{0};
+  hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&attention_few_kernel<D, NQ>), few_lds<D, NQ>(), done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attention_few_kernel<D, NQ>), grid, dim3(64 * FEW_WAVES), (few_lds<D, NQ>()), st, a);
+  return hipGetLastError();
+}
+
 template <int D>
 static hipError_t launch_attention_d(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   const dim3 grid((unsigned)(a.c.H * p.units));
@@ -1151,10 +1173,11 @@ static hipError_t launch_attention_d(const AttnArgs& a, const AttnPlan& p, hipSt
     hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&attention_many_kernel<D>), lds, done);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(attention_many_kernel<D>, grid, dim3(64 * MANY_WAVES), lds, st, a);
-  } else if (p.nq == 1) {
-    hipLaunchKernelGGL((attention_few_kernel<D, 1>), grid, dim3(256), 0, st, a);
   } else {
-    if constexpr (D <= 128) hipLaunchKernelGGL((attention_few_kernel<D, 2>), grid, dim3(256), 0, st, a);
+    hipError_t e = hipSuccess;
+    if (p.nq == 1) e = launch_few<D, 1>(a, grid, st);
+    else if constexpr (D <= 128) e = launch_few<D, 2>(a, grid, st);
+    if (e != hipSuccess) return e;
   }
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.target) {
