@@ -101,8 +101,8 @@ mxq_status cache_args(const char* fn, const mxq_cache* cache, const int32_t* blo
     return fail(MXQ_EUNSUPPORTED, "%s: head_dim must be 64, 128 or 256 (head_dim=%d)", fn, D);
   if (P < 16 || P > 1024 || (P & (P - 1)))
     return fail(MXQ_EUNSUPPORTED, "%s: page_size must be a power of two from 16 to 1024 (page_size=%d)", fn, P);
-  if (cache->num_heads < 1 || cache->num_heads > 65535)
-    return fail(MXQ_EINVAL, "%s: num_heads must be 1 to 65535", fn);
+  if (cache->num_heads < 1 || cache->num_heads > 32767)
+    return fail(MXQ_EINVAL, "%s: num_heads must be 1 to 32767", fn);
   if (!q_offsets && tokens != num_requests)
     return fail(MXQ_EINVAL, "%s: without q_offsets there is one row per request (tokens=%lld, requests=%lld)", fn,
                 (long long)tokens, (long long)num_requests);
@@ -253,6 +253,7 @@ mxq_status nvfp4_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_
   a.o_head = out_head_stride;
   a.lse = lse;
   a.target = p.target;
+  a.coarse = p.coarse;
   if (need) {
     const int64_t rows = p.units * H * p.ct;
     a.part_o = static_cast<float*>(workspace);

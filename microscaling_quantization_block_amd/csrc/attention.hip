@@ -130,14 +130,14 @@ __device__ __forceinline__ uint32_t pair_nibbles(uint32_t a, uint32_t b, bool od
 // ------------------------------------------------------------------- work units
 //
 // A unit is a column tile of one request and a chunk of its context; a
-// workgroup takes a unit for one KV head.  All chunks are about equally long
-// (of all requests together, `target` of them), so that a batch of ragged
-// lengths fills the chip evenly; with target 0 a request is one chunk.  The
+// workgroup takes a unit for one KV head.  All chunks are about equally long,
+// of all requests together, so that a batch of ragged lengths fills the chip
+// evenly; with target 0 a request is one chunk.  The
 // lengths are on the device: every workgroup finds its unit by scanning them.
 struct Unit {
   int b, ct, chunk, chunks;     // request, column tile, chunk of its chunks
   int q_begin, q_len, L;
-  int64_t base;                 // first unit of the request
+  int base;                     // first unit of the request
 };
 
 struct RequestSize {
@@ -163,7 +163,7 @@ __device__ __forceinline__ RequestSize request_size(const AttnArgs& a, int64_t b
   return r;
 }
 
-__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+__device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int s = 1; s < 64; s *= 2) v += __shfl_xor(v, s, 64);
   return v;
@@ -175,41 +175,45 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int u, int CT, int 
   RequestSize r = request_size(a, lane, CT);
   int chunk = 0x7FFFFFFF;
   if (a.target) {
-    int64_t work = (int64_t)r.cts * r.tiles;
+    float work = (float)r.cts * (float)r.tiles;
     for (int64_t b = 64 + lane; b < B; b += 64) {
       const RequestSize x = request_size(a, b, CT);
-      work += (int64_t)x.cts * x.tiles;
+      work += (float)x.cts * (float)x.tiles;
     }
     work = wave_sum(work);
-    const int64_t c = (work + a.target - 1) / a.target;
-    chunk = (int)(c < MIN_CHUNK ? MIN_CHUNK : c > 0x7FFFFFFF ? 0x7FFFFFFF : c);
+    // never more than `target` chunks beside one per column tile (the grid's
+    // bound; the sum is rounded, hence the margin); fewer, `coarse`, as long as
+    // that leaves no chunk longer than LONG_CHUNK
+    const float fine = work * (1.00001f / (float)a.target), coarse = work / (float)a.coarse;
+    const float c = fmaxf(fine, fminf(coarse, (float)LONG_CHUNK));
+    chunk = max(MIN_CHUNK, c < 1e9f ? (int)c + 1 : 0x7FFFFFFF);
   }
-  int64_t base = 0;
+  int base = 0;
   for (int64_t b0 = 0; b0 < B; b0 += 64) {
     if (b0) r = request_size(a, b0 + lane, CT);
     const int chunks = r.tiles > chunk ? (r.tiles + chunk - 1) / chunk : 1;
-    const int64_t mine = (int64_t)r.cts * chunks;
-    int64_t incl = mine;
+    const int mine = r.cts * chunks;           // the host bounds the sum
+    int incl = mine;
 #pragma unroll
     for (int s = 1; s < 64; s *= 2) {
-      const int64_t o = __shfl_up(incl, s, 64);
+      const int o = __shfl_up(incl, s, 64);
       if (lane >= s) incl += o;
     }
     const uint64_t hit = __ballot(base + incl > u);
     if (hit) {
       const int src = __builtin_ctzll(hit);
       out.b = __builtin_amdgcn_readfirstlane((int)b0 + src);
-      out.base = base + __shfl(incl - mine, src, 64);
+      out.base = base + __builtin_amdgcn_readlane(incl - mine, src);
       out.chunks = __builtin_amdgcn_readlane(chunks, src);
       out.q_begin = __builtin_amdgcn_readlane(r.q_begin, src);
       out.q_len = __builtin_amdgcn_readlane(r.q_len, src);
       out.L = __builtin_amdgcn_readlane(r.L, src);
-      const int i = __builtin_amdgcn_readfirstlane((int)(u - out.base));
+      const int i = __builtin_amdgcn_readfirstlane(u - out.base);
       out.ct = i / out.chunks;
       out.chunk = i - out.ct * out.chunks;
       return true;
     }
-    base += __shfl(incl, 63, 64);
+    base += __builtin_amdgcn_readlane(incl, 63);
   }
   return false;
 }
@@ -403,7 +407,7 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, const Unit& u, int6
 // The join finds a request's units by this.
 __device__ __forceinline__ void store_index(const AttnArgs& a, const Unit& u, int h) {
   if (a.target && u.ct == 0 && u.chunk == 0 && h == 0 && threadIdx.x == 0)
-    a.part_index[u.b] = make_int2((int)u.base, u.chunks);
+    a.part_index[u.b] = make_int2(u.base, u.chunks);
 }
 
 // ------------------------------------------------------- raw tiles through LDS
@@ -1108,7 +1112,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int CT)
   const int h = (int)(head / a.G);
   const int64_t j = (tq - (a.c.q_offsets ? a.c.q_offsets[b] : tq)) * a.G + (head - (int64_t)h * a.G);
   const int64_t stride = (int64_t)a.c.H * CT;  // of a chunk
-  const int64_t first = ((ix.x + j / CT * chunks) * a.c.H + h) * CT + j % CT;
+  const int64_t first = (((int64_t)ix.x + j / CT * chunks) * a.c.H + h) * CT + j % CT;
   float mx = NEG_INF;
   for (int k = lane; k < chunks; k += 64) mx = fmaxf(mx, a.part_lse[first + k * stride]);
 #pragma unroll

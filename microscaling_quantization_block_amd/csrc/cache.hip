@@ -21,14 +21,12 @@ template <int D>
 __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
   constexpr int L = D / 8;                     // lanes of a row
   const CacheArgs& c = a.c;
-  const int64_t rows = a.T * c.H * 2;
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+  // blockIdx.y: (head, K or V); a workgroup's rows are neighbouring tokens
+  const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
   const int lane = threadIdx.x & (L - 1);
-  if (row >= rows) return;                     // whole rows leave: the lane exchanges below stay inside a row
-  // a row's index is (head, K or V, token): neighbours are tokens of one head
-  const int64_t t = row % a.T, hv = row / a.T;
-  const bool is_v = hv & 1;
-  const int64_t h = hv >> 1;
+  if (t >= a.T) return;                        // whole rows leave: the lane exchanges below stay inside a row
+  const bool is_v = blockIdx.y & 1;
+  const int64_t h = blockIdx.y >> 1;
   const int64_t b = request_of(c, t);
   if (b < 0) return;
   const int64_t q_end = c.q_offsets ? c.q_offsets[b + 1] : t + 1;
@@ -76,8 +74,8 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
 }
 
 hipError_t launch_cache_append(const AppendArgs& a, hipStream_t st) {
-  const int64_t threads = a.T * a.c.H * 2 * (a.c.D / 8);
-  const dim3 grid((unsigned)((threads + 255) / 256));
+  const int64_t rows = 256 / (a.c.D / 8);      // of a workgroup
+  const dim3 grid((unsigned)((a.T + rows - 1) / rows), (unsigned)(2 * a.c.H));
   if (a.c.D == 64) hipLaunchKernelGGL(cache_append_kernel<64>, grid, dim3(256), 0, st, a);
   else if (a.c.D == 128) hipLaunchKernelGGL(cache_append_kernel<128>, grid, dim3(256), 0, st, a);
   else hipLaunchKernelGGL(cache_append_kernel<256>, grid, dim3(256), 0, st, a);

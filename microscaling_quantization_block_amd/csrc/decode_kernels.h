@@ -63,16 +63,22 @@ struct AttnArgs {
   // unit and its chunks
   float *part_o, *part_lse;
   int2* part_index;
-  int target;                   // chunks aimed at in all; 0: a request's context is one chunk
+  // chunks of all requests: at most `target` beside one per column tile, `coarse` if that
+  // makes none longer than LONG_CHUNK; target 0: a request's context is one chunk
+  int target, coarse;
 };
 
 constexpr int MANY_WAVES = 8;                  // waves of a workgroup with many columns
 constexpr int MIN_CHUNK = 8;                   // 32-token tiles of the shortest chunk
+// Two workgroups per compute unit as long as a chunk stays below 2048 tokens,
+// else six: 64 contexts up to 4096 took 53.8, 56.4, 57.7 us with 512, 768, 1536
+// workgroups aimed at, four contexts up to 131071 110, 104, 93.5.
+constexpr int LONG_CHUNK = 64;
 
 // How a call is cut: column tiles of ct (query, head) pairs, and the number
 // of work units (a bound).
 struct AttnPlan {
-  int nq, waves, ct, target;
+  int nq, waves, ct, target, coarse;
   int64_t units;
 };
 inline AttnPlan plan_attention(int64_t B, int64_t T, int H, int G, int D, int64_t max_context, bool ragged) {
@@ -86,9 +92,10 @@ inline AttnPlan plan_attention(int64_t B, int64_t T, int H, int G, int D, int64_
   p.ct = p.waves ? 32 * p.waves : 16 * p.nq;
   const int64_t tiles = ragged ? T * G / p.ct + B : B * ((G + p.ct - 1) / p.ct);
   // workgroups aimed at
-  const int64_t want = p.waves ? 256 : 768;
+  const int64_t want = p.waves ? 256 : 1536, few = p.waves ? 256 : 512;
   const int64_t most = (max_context + 32 * MIN_CHUNK - 1) / (32 * MIN_CHUNK);   // chunks of the longest context
   p.target = most <= 2 || tiles * H >= 4 * want ? 0 : (int)((want + H - 1) / H);
+  p.coarse = (int)((few + H - 1) / H);
   const int64_t bound = tiles * most;
   p.units = p.target ? (tiles + p.target < bound ? tiles + p.target : bound) : tiles;
   return p;
