@@ -188,7 +188,8 @@ mxq_status nvfp4_cache_append(const uint16_t* k, int64_t k_token_stride, int64_t
   if ((s = check_rows(fn, "k", k, k_token_stride, k_head_stride, D)) != MXQ_OK) return s;
   if ((s = check_rows(fn, "v", v, v_token_stride, v_head_stride, D)) != MXQ_OK) return s;
   if (!aligned16(k_dq) || !aligned16(v_dq)) return fail(MXQ_EALIGN, "%s: k_dq and v_dq 16-byte aligned", fn);
-  if (tokens * cache->num_heads * 2 * (D / 8) >= 2 * I31 - 256)
+  const int64_t wg_rows = 2048 / D;            // a workgroup's; its 256 lanes times the grid stay below 2^32
+  if ((tokens + wg_rows - 1) / wg_rows * 2 * cache->num_heads >= I31 / 128)
     return fail(MXQ_EUNSUPPORTED, "%s: too many rows for one call", fn);
   a.k = k;
   a.v = v;
