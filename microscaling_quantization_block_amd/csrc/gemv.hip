@@ -6,21 +6,27 @@
 // binary32.  S leaves the sum and multiplies it once, in binary32; one
 // rounding to BF16 ends the chain.
 //
-// One workgroup owns 16 RT weight rows (with SwiGLU as many gate rows and
-// their up rows) and all of K; its waves take 256-wide K chunks in turn (a whole
-// 128-byte line of codes per row) and their partial tiles meet in LDS, so there
-// are many loads in flight for a matrix with few rows and no second launch.
-// The weights are the left operand: lane (c, g) = (lane % 16, lane / 16) reads
-// 32 bytes, the codes k0 + 64 g .. + 63 of row c, with their four scales in one
-// word, and feeds them to eight matrix instructions eight at a time; x is read
-// in the same order, so k is permuted alike on both sides and nothing is
-// shuffled.  RT > 1 because x comes through the caches: 16 rows of x are four
-// times the bytes of 16 rows of codes.
+// Three kernels; all are bound by the weights' bytes (one row through 4096 x
+// 14336: 33 MB in 10.2 us; 13 rows through 24576 x 4096: 57 MB in 20.9 us, 2.7
+// TB/s, where a large copy has 4.8), the short ones by the latency of one load
+// and of the join of the partial sums.
 //
-// Bound by memory: the codes are read once.  A chunk's loads are in flight
-// while the one before it is multiplied; no load in the loop depends on a
-// branch (lanes without a row of x read some row, whose column is dropped at
-// the end), so the waits count them.
+// This first one takes any shape and any number of rows.  A workgroup owns 16 RT
+// weight rows (with SwiGLU as many gate rows and their up rows) and all of K;
+// its waves take 256-wide K chunks in turn (a whole 128-byte line of codes per
+// row) and their partial tiles meet in LDS, so there are many loads in flight
+// for a matrix with few rows and no second launch.  The weights are the left
+// operand: lane (c, g) = (lane % 16, lane / 16) reads 32 bytes, the codes k0 +
+// 64 g .. + 63 of row c, with their four scales in one word, and feeds them to
+// eight matrix instructions eight at a time; x is read in the same order, so k
+// is permuted alike on both sides and nothing is shuffled.  (Lanes g next to
+// each other along K, in 8-byte pieces, touch half as many lines per load but
+// need more loads: 23.4 us against 20.7 for 8 rows through 4096 x 14336.)
+// R > 1 because x comes through the caches: 16 rows of x are four times the
+// bytes of 16 rows of codes.  A chunk's loads are in flight while the one
+// before it is multiplied; no load in the loop depends on a branch (lanes
+// without a row of x read some row, whose column is dropped at the end), so the
+// waits count them.
 
 #include "mxq_device.h"
 #include "decode_kernels.h"
@@ -55,7 +61,7 @@ __device__ __forceinline__ int64_t gemv_scale_offset(int64_t row, int64_t b, int
 // R tiles of 16 weight rows (with SwiGLU tile 2 t holds gate rows and tile
 // 2 t + 1 their up rows), MT tiles of 16 rows of x.
 template <int SL, bool SWI, int R, int MT>
-__global__ __launch_bounds__(R == 1 ? 1024 : 512) void gemv_kernel(GemvArgs a) {
+__global__ __launch_bounds__(R == 1 && MT == 1 ? 1024 : 512) void gemv_kernel(GemvArgs a) {
   constexpr int RT = SWI ? R / 2 : R;          // tiles of output columns
   extern __shared__ float red[];               // [waves][R][MT * 16 columns m][16 rows n]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
@@ -213,7 +219,7 @@ template <int SL, bool SWI, int R, int MT>
 static hipError_t launch_gemv_as(const GemvArgs& a, hipStream_t st) {
   constexpr int RT = SWI ? R / 2 : R;
   // a wave per chunk, as far as there is room
-  const int chunks = (int)((a.K + 255) >> 8), most = R == 1 ? 16 : 8, per = (chunks + most - 1) / most;
+  const int chunks = (int)((a.K + 255) >> 8), most = R == 1 && MT == 1 ? 16 : 8, per = (chunks + most - 1) / most;
   const int nw = (chunks + per - 1) / per;
   const dim3 grid((unsigned)((a.N + 16 * RT - 1) / (16 * RT)), (unsigned)(a.num_groups ? a.num_groups : 1));
   const size_t lds = (size_t)nw * R * MT * 256 * sizeof(float);
@@ -223,8 +229,8 @@ static hipError_t launch_gemv_as(const GemvArgs& a, hipStream_t st) {
 
 // ------------------------------------------------------------------ a few rows
 //
-// For up to three rows of x or so per matrix the matrix instruction has little
-// to do, and its operand layout reads 16 rows at once, 16 bytes each, which
+// For one or two rows of x per matrix the matrix instruction has little to do,
+// and its operand layout reads 16 rows at once, 16 bytes each, which
 // the memory path takes apart.  Here the lanes lie along K: a lane holds 32
 // codes of a row, 16 bytes, and a load of a wave is one kilobyte of one row
 // (or of 64 / LPR rows where K is short).  A wave reads 16 such pieces of
@@ -239,7 +245,6 @@ static hipError_t launch_gemv_as(const GemvArgs& a, hipStream_t st) {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int DOT_ITEMS = 16;
-constexpr int MMX = 2;
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {
@@ -277,7 +282,8 @@ __device__ __forceinline__ float dot8(uint32_t w, uint4 x, float acc) {
   return acc;
 }
 
-// MM rows of x at a time; ks waves of a workgroup share a row's K.
+// MM rows of x at a time (one where no matrix has more on average: two need 32
+// more registers); ks waves of a workgroup share a row's K.
 template <int SL, bool SWI, int LPR, int MM>
 __global__ __launch_bounds__(512, MM == 1 ? 4 : 3) void gemv_dot_kernel(GemvArgs a, int ks) {
   constexpr int ITEMS = DOT_ITEMS, RPL = 64 / LPR;             // rows of a load
@@ -329,8 +335,8 @@ __global__ __launch_bounds__(512, MM == 1 ? 4 : 3) void gemv_dot_kernel(GemvArgs
       const uint8_t* p = scales + ((row >> 5) * (B >> 2) + (b0 >> 2)) * 128 + (row & 31) * 4;
 #pragma unroll
       for (int i = 0; i < RUN; i += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
-        const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+        uint32_t word[4];                      // scales may lie at any address
+        __builtin_memcpy(word, p + 4 * i, 16);
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[r * RUN + i + j] = word[j] >> (8 * (b0 & 3));
       }
@@ -403,12 +409,12 @@ static hipError_t launch_dot_as(const GemvArgs& a, hipStream_t st) {
 
 template <int SL, bool SWI>
 static hipError_t launch_dot_sl(const GemvArgs& a, bool one, hipStream_t st) {
-  if (a.K <= 512) return one ? launch_dot_as<SL, SWI, 16, 1>(a, st) : launch_dot_as<SL, SWI, 16, MMX>(a, st);
-  if (a.K <= 1024) return one ? launch_dot_as<SL, SWI, 32, 1>(a, st) : launch_dot_as<SL, SWI, 32, MMX>(a, st);
-  return one ? launch_dot_as<SL, SWI, 64, 1>(a, st) : launch_dot_as<SL, SWI, 64, MMX>(a, st);
+  if (a.K <= 512) return one ? launch_dot_as<SL, SWI, 16, 1>(a, st) : launch_dot_as<SL, SWI, 16, 2>(a, st);
+  if (a.K <= 1024) return one ? launch_dot_as<SL, SWI, 32, 1>(a, st) : launch_dot_as<SL, SWI, 32, 2>(a, st);
+  return one ? launch_dot_as<SL, SWI, 64, 1>(a, st) : launch_dot_as<SL, SWI, 64, 2>(a, st);
 }
 
-// --------------------------------------------------------------- up to 16 rows
+// ------------------------------------------------------------ x held in registers
 //
 // The matrix instruction again, for K up to 4096: a wave keeps its one or two
 // chunks of x in registers (read once) and streams weight tiles past them, so
@@ -573,22 +579,38 @@ static bool can_stream(const GemvArgs& a) {
   return a.K % 64 == 0 && a.K <= 4096 && a.ld_w % 16 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0;
 }
 
+// Which kernel, by the rows per matrix on average and by the 16-row weight tiles
+// of all matrices.  Measured, weights from memory:
+//   lanes along K up to two rows: 2 rows through 4096 x 14336 12.9 us, tiles 16.6;
+//     3 rows through 24576 x 4096 23.4 us, streamed 18.4.
+//   streamed up to 16 rows: 8 rows through 4096 x 4096 8.3 us; lanes along K
+//     16.8.  With more rows the weights come again for each 16 of them, from a
+//     cache, which pays where x is long and there are many tiles: 32 rows
+//     through 24576 x 4096 37.7 us, tiles 50.0; but 32 rows through 4096 x 4096
+//     16.3 and 16.1, 64 through sixteen 2048 x 768 24.4 and 16.9.
+//   tiles for the rest: R tiles of a workgroup share its x, as few as let all
+//     workgroups run at once.  8 rows, R = 1, 2, 4: 4096 x 14336 20.7, 22.0,
+//     33.4 us; 8192 x 8192 31, 17.3, 31; 16384 x 5120 36.1, 21.8, 19.1.
 template <int SL, bool SWI>
 static hipError_t launch_gemv_sl(const GemvArgs& a, hipStream_t st) {
   const int64_t groups = a.num_groups ? a.num_groups : 1;
-  const int64_t rows = (a.M + groups - 1) / groups;            // of x, per matrix
-  const int64_t tiles = (a.N + 15) / 16 * groups;
-  if (rows <= 3 && a.K >= 32 && a.K <= 16384) return launch_dot_sl<SL, SWI>(a, rows == 1, st);
-  if (rows <= 16 && can_stream(a)) {
+  const int64_t rows = (a.M + groups - 1) / groups;
+  const int64_t tiles = (a.N + 15) / 16 * (SWI ? 2 : 1) * groups;
+  if (rows <= 2 && a.K >= 32 && a.K <= 16384) return launch_dot_sl<SL, SWI>(a, rows == 1, st);
+  if (can_stream(a) && (rows <= 16 || (tiles > 512 && a.K > 2048))) {
     const int chunks = (int)((a.K + 255) >> 8);
     if (chunks > 8) return launch_stream_as<SL, SWI, 2, 3>(a, (chunks + 1) / 2, st);
     return chunks > 4 ? launch_stream_as<SL, SWI, 1, 3>(a, chunks, st) : launch_stream_as<SL, SWI, 1, 2>(a, chunks, st);
   }
-  if (rows > 16) return launch_gemv_as<SL, SWI, 2, 2>(a, st);
-  if (tiles >= 2048) return launch_gemv_as<SL, SWI, 4, 1>(a, st);
-  if (SWI || tiles >= 1024) return launch_gemv_as<SL, SWI, 2, 1>(a, st);
-  if constexpr (!SWI) return launch_gemv_as<SL, SWI, 1, 1>(a, st);
-  return hipErrorInvalidValue;                 // not reached
+  const int R = tiles <= 256 ? 1 : tiles <= 512 ? 2 : 4;
+  if (rows > 16) {
+    if constexpr (!SWI)
+      if (R == 1) return launch_gemv_as<SL, SWI, 1, 2>(a, st);
+    return R == 4 ? launch_gemv_as<SL, SWI, 4, 2>(a, st) : launch_gemv_as<SL, SWI, 2, 2>(a, st);
+  }
+  if constexpr (!SWI)
+    if (R == 1) return launch_gemv_as<SL, SWI, 1, 1>(a, st);
+  return R == 4 ? launch_gemv_as<SL, SWI, 4, 1>(a, st) : launch_gemv_as<SL, SWI, 2, 1>(a, st);
 }
 
 hipError_t launch_nvfp4_gemv(const GemvArgs& a, GemvScales layout, bool swiglu, hipStream_t st) {

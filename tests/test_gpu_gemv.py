@@ -154,3 +154,90 @@ def test_equal_calls_give_equal_bits():
     first = m.nvfp4_gemv(x, w, 9, 512, 4096)
     for _ in range(3):
         assert torch.equal(first, m.nvfp4_gemv(x, w, 9, 512, 4096))
+
+
+@pytest.mark.parametrize("m_rows,n,k", [
+    (3, 70, 14336), (9, 300, 8208), (16, 64, 12288),             # long K, few tiles; K no multiple of 64
+    (5, 4200, 80), (6, 8200, 96), (11, 24600, 48),               # 263, 513 and 1538 tiles of short K
+    (18, 4200, 80), (35, 8208, 144),                             # the same with more than 16 rows
+    (20, 8208, 2112), (33, 8224, 4096)])                         # x in registers, 16 rows after 16 rows
+def test_tile_counts(m_rows, n, k):
+    _dense("gemv", m_rows, n, k, "row", "linear", n + k)
+
+
+@pytest.mark.parametrize("m_rows,n,k", [(3, 40, 14336), (5, 2104, 80), (9, 4120, 48), (18, 2104, 80), (35, 4104, 144),
+                                        (20, 4112, 2112)])
+def test_tile_counts_swiglu(m_rows, n, k):
+    _dense("swiglu", m_rows, n, k, "row", "linear", n + k)
+
+
+@pytest.mark.parametrize("block,layout", [("tile", "linear"), ("row", "mfma")])
+@pytest.mark.parametrize("m_rows,n,k", [(4, 96, 8192), (18, 4224, 320), (10, 4224, 4160), (20, 8224, 2112)])
+def test_tile_counts_of_other_scales(block, layout, m_rows, n, k):
+    _dense("gemv", m_rows, n, k, block, layout, n + k)
+
+
+@pytest.mark.parametrize("m_rows", [1, 2, 5, 20])
+@pytest.mark.parametrize("block,layout", [("row", "linear"), ("row", "mfma"), ("tile", "linear")])
+@pytest.mark.parametrize("op", ["gemv", "swiglu"])
+def test_strided_weight_and_scales_at_any_address(op, block, layout, m_rows):
+    """Codes as a column slice of a wider tensor, the scales one byte behind an aligned address."""
+    m, rng = _m(), np.random.default_rng(m_rows)
+    n, k = 64, 192
+    nw = 2 * n if op == "swiglu" else n
+    w = R.Weight(rng, nw, k, block, layout)
+    wide = torch.randint(0, 256, (nw, k // 2 + 64), dtype=torch.uint8, device="cuda")
+    wide[:, 32:32 + k // 2] = torch.from_numpy(w.codes[0]).cuda()
+    flat = torch.from_numpy(np.ascontiguousarray(w.scales)).reshape(-1)
+    room = torch.full((flat.numel() + 8,), 0x7F, dtype=torch.uint8, device="cuda")      # 0x7F: NaN
+    room[1:1 + flat.numel()] = flat.cuda()
+    op_w = m.Operand(m.Format.NVFP4, wide[:, 32:32 + k // 2], room[1:1 + flat.numel()].view(w.scales.shape),
+                     torch.from_numpy(w.S).cuda(), block=m.Block.TILE if block == "tile" else m.Block.ROW,
+                     gs=m.GScale.PER_TENSOR, layout=m.Layout.MFMA if layout == "mfma" else m.Layout.LINEAR)
+    x = _x(rng, m_rows, k)
+    say(f"strided weight {op} {block} {layout} {m_rows}")
+    fn = m.nvfp4_gemv if op == "gemv" else m.nvfp4_gemv_swiglu
+    got = F.bf16_bits_to_f64(from_dev_bf16(fn(to_dev_bf16(x), op_w, m_rows, n, k)))
+    xv = F.bf16_bits_to_f64(x)
+    ref, tol = R.gemv_ref(xv, w.dq[0]) if op == "gemv" else R.swiglu_ref(xv, w.dq[0][:n], w.dq[0][n:])
+    _check(got, ref, tol, (op, block, layout, m_rows))
+
+
+@pytest.mark.parametrize("counts", [[20, 0, 33], [1, 2, 40], [0, 19]])
+@pytest.mark.parametrize("k", [80, 192, 2112])
+def test_uneven_groups(k, counts):
+    """One group far above the average the kernel was chosen by."""
+    m, rng = _m(), np.random.default_rng(k + sum(counts))
+    n, e = 96, len(counts)
+    w = R.Weight(rng, n, k, groups=e)
+    rows = sum(counts)
+    x = _x(rng, rows, k)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    say(f"uneven groups {k} {counts}")
+    got = F.bf16_bits_to_f64(from_dev_bf16(m.nvfp4_gemv(to_dev_bf16(x), w.operand(m, torch), rows, n, k,
+                                                        group_row_offsets=torch.from_numpy(off).cuda())))
+    for g in range(e):
+        r = slice(off[g], off[g + 1])
+        ref, tol = R.gemv_ref(F.bf16_bits_to_f64(x)[r], w.dq[g])
+        _check(got[r], ref, tol, (k, counts, g))
+
+
+@pytest.mark.parametrize("m_rows,n,k", [(1, 40, 256), (2, 40, 256), (7, 40, 256), (7, 40, 272), (20, 40, 256)])
+def test_infinite_and_nan_rows_stay_by_themselves(m_rows, n, k):
+    """A row of x with an infinity or a NaN spoils its own row of y only; so does a row nobody asked for."""
+    m, rng = _m(), np.random.default_rng(k + m_rows)
+    w = R.Weight(rng, n, k)
+    op = w.operand(m, torch)
+    x = to_dev_bf16(_x(rng, m_rows + 2, k))
+    want = m.nvfp4_gemv(x[:m_rows], op, m_rows, n, k)
+    x[m_rows:] = float("nan")
+    bad = m_rows - 1
+    if m_rows > 1:
+        x[bad, 5] = float("inf")
+        x[bad, 9] = float("nan")
+    say(f"infinite rows {m_rows} {k}")
+    got = m.nvfp4_gemv(x[:m_rows], op, m_rows, n, k)
+    good = slice(0, bad if m_rows > 1 else 1)
+    assert torch.equal(got[good], want[good])
+    if m_rows > 1:
+        assert got[bad].isnan().all()
