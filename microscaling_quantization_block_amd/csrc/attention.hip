@@ -4,26 +4,34 @@
 // context, o = sum_t softmax(x)_t v_t, with k_t = value(c) s_b S_t.  Computed in
 // one pass over the cache with the running maximum m and sum l of the softmax.
 //
-// The products run on the 16x16x32 FP16 matrix instruction.  value(c) s_b is
-// an FP16 number (at most six significant bits, 2^-10 .. 2688), so K and V
-// enter exactly; a query row is scaled by a power of two to have its largest
-// element in [2^13, 2^14), which keeps its eight significant bits down to 2^-27
-// of that element.  S of K multiplies the logit.  S of V multiplies the
-// weight: w_t = p_t S_t / Sref 2^15 with Sref a running power of two above
-// every S_t seen, rounded to FP16 (11 bits, 29 binades before it turns
-// subnormal).  Sums, maxima and logits are binary32.
+// The products run on the FP16 matrix instructions.  value(c) s_b is an FP16
+// number (at most six significant bits, 2^-10 .. 2688), so K's codes enter
+// exactly; a query row is scaled by a power of two to have its largest element
+// in [2^13, 2^14), which keeps its eight significant bits down to 2^-27 of that
+// element.  S of K multiplies the logit, in binary32.  S of V is brought near
+// one by Sref, a running power of two above every S_t seen, and goes to the
+// weights w_t = p_t S_t / Sref (few columns: fewer weights than values) or to the
+// values (many columns: the dequantized tile is shared); either is one rounding
+// to FP16, 2^-11 relative.  Sums, maxima and logits are binary32, and l sums
+// the exponentials before they are rounded.
 //
-// Orientation: logits are computed transposed, X^T = K Q^T (A = 16 tokens, B = 16
-// query columns), and the output too, O^T = V^T W^T.  A lane then holds one
-// column (lane % 16) in both, so the softmax statistics and every rescaling
-// are lane-local but for one exchange over the four lane groups, and the
-// weights W leave the first product in the register layout the second one
-// reads: the order of the 32 contracted tokens is permuted alike on both
-// sides.  Lane (c, g) reads D / 8 contiguous code bytes of token c for K (the
-// D / 4 values from g D / 4 on; q is read in that order), and for V D / 32
-// bytes of each of the tokens 4 g .. 4 g + 3 of both 16-token halves; a pair of
-// tokens' nibbles is interleaved so that one conversion gives two
-// neighbouring contraction elements.
+// Orientation: logits are computed transposed, X^T = K Q^T (A = tokens, B = query
+// columns), and the output too, O^T = V^T W^T.  A lane then holds one column in
+// both, so the softmax statistics and every rescaling are lane-local but for
+// one exchange over the lane groups, and the weights W leave the first product
+// in the register layout the second one reads: the order of the contracted
+// tokens is permuted alike on both sides.  K's D values are contracted in the
+// order the lanes hold them, q in the same; a pair of tokens' nibbles of V is
+// interleaved so that one conversion gives two neighbouring contraction
+// elements.
+//
+// Two kernels, by the query columns (row, head of the KV head's group) of a
+// request, and a join where contexts are split.  With few columns the cache's
+// bytes bound it: 64 requests of up to 4096 tokens, 177 MB, 55.6 us (3.2 TB/s);
+// four of up to 131071, 393 MB, 91.7 us (4.3 TB/s, a large copy has 4.8).  With
+// many the matrix and vector units do: prompt chunks of 2048 rows behind 8192
+// tokens, 437 GF, 784 us (558 TF/s).  A single short request is latency: 11.7
+// us, the join's launch included.
 
 #include "cache_device.h"
 #include "mxq_kernels.h"
