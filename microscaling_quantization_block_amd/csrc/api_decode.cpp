@@ -206,6 +206,8 @@ mxq_status nvfp4_cache_append(const uint16_t* k, int64_t k_token_stride, int64_t
 int64_t nvfp4_attention_workspace(int64_t tokens, int32_t num_q_heads, int32_t num_heads, int32_t head_dim,
                                   int32_t page_size, int64_t table_width, int64_t num_requests, int32_t ragged) {
   if (tokens <= 0 || num_requests <= 0 || num_heads <= 0 || num_q_heads < num_heads || head_dim <= 0) return 0;
+  if (tokens >= I31 || num_requests >= I31 || page_size <= 0 || table_width < 0 || table_width > I31 / 2 / page_size)
+    return 0;                                  // nvfp4_attention refuses these
   const mxq::AttnPlan p = mxq::plan_attention(num_requests, tokens, num_heads, num_q_heads / num_heads, head_dim,
                                               table_width * page_size, ragged != 0);
   return mxq::attention_workspace(p, num_requests, num_heads, head_dim);
@@ -248,7 +250,7 @@ mxq_status nvfp4_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_
   a.Hq = num_q_heads;
   a.G = num_q_heads / H;
   a.scale_log2 = scale * 1.44269504088896340736f;
-  a.window = window;
+  a.window = window < I31 ? window : 0;        // positions lie below 2^31: it holds them all
   a.out = out;
   a.o_token = out_token_stride;
   a.o_head = out_head_stride;

@@ -241,7 +241,7 @@ def _check_requests(cache, block_table, seq_lens, q_offsets, rows):
         _check_index(q_offsets, "q_offsets", n + 1, dev)
     elif rows != n:
         raise ValueError(f"without q_offsets there is one row per request ({rows} rows, {n} requests)")
-    return dev, n, width, block_table.stride(0)
+    return dev, n, width, block_table.stride(0) if n > 1 else width
 
 
 def _check_rows(t, name, heads, d, rows, dev):

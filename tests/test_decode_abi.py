@@ -142,6 +142,9 @@ def test_workspace_follows_the_shapes():
     assert ws(2, 32, 8, 128, 64, 2048, 2, False) > 0                  # two long contexts are split
     assert ws(2, 32, 8, 128, 64, 2048, 2, True) > 0
     assert ws(2, 32, 8, 128, 64, 1, 2, False) == 0                    # one page: nothing to split
+    for bad in ((1 << 40, 32, 8, 128, 64, 2048, 2), (2, 32, 8, 128, 64, 1 << 60, 2), (2, 32, 8, 128, 0, 2048, 2),
+                (2, 32, 8, 128, 64, -1, 2), (2, 32, 8, 128, 64, 2048, 1 << 62)):
+        assert ws(*bad, False) == 0                                   # the call refuses these
 
 
 def test_binding_refuses_before_the_library_is_called():

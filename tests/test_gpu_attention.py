@@ -207,3 +207,69 @@ def test_empty_calls():
     out = m.nvfp4_attention(q, cache, torch.empty((0, 4), dtype=torch.int32, device="cuda"),
                             torch.empty(0, dtype=torch.int32, device="cuda"))
     assert out.shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("news", [[1, 1], [3, 70]])
+def test_windows_wider_than_any_context(news):
+    p = Problem(11, 64, 1, 2, 16, [300, 90], news)
+    a, la = p.run()
+    for p.window in (1 << 31, (1 << 32) + 3, (1 << 63) - 1):
+        b, lb = p.run()
+        assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("lens,news", [([40, 33], [3, 2]), ([300, 90], [1, 70]), ([3000, 40], [1, 1])])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_spoilt_query_row_stays_by_itself(lens, news, bad):
+    """An infinity or a NaN in one row and head leaves every other row and head as it was."""
+    p = Problem(12, 128, 1, 4, 16, lens, news)
+    a, la = p.run()
+    q = to_dev_bf16(p.q)
+    row, head = p.total - 1, 2
+    q[row, head, 7] = bad
+    b, lb = p.run(q=q)
+    keep = torch.ones(p.total, 4, dtype=torch.bool, device="cuda")
+    keep[row, head] = False
+    assert torch.equal(a[keep], b[keep]) and torch.equal(la[keep], lb[keep])
+
+
+@pytest.mark.parametrize("new", [1, 90])
+def test_shared_pages_and_a_page_named_twice(new):
+    """Two requests over the same pages answer alike; a table that names a page twice reads it twice."""
+    p = Problem(13, 64, 2, 2, 16, [128], [new])
+    table = np.concatenate([p.table, p.table])
+    q = to_dev_bf16(np.concatenate([p.q, p.q]))
+    m = _m()
+    cache = p.cache.device(m, torch)
+    say(f"shared pages {new}")
+    out = m.nvfp4_attention(q, cache, _dev(table), _dev([128, 128]), q_offsets=_dev([0, new, 2 * new]))
+    assert torch.equal(out[:new], out[new:])
+    p.check(out[:new], p.run()[1])
+    p.table = np.concatenate([p.table[:, :4], p.table[:, :4]], 1)
+    p.k = [np.concatenate([x[:, :64], x[:, :64]], 1) for x in p.k]
+    p.v = [np.concatenate([x[:, :64], x[:, :64]], 1) for x in p.v]
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("new", [1, 40, 300])
+def test_pages_far_apart(new):
+    """Pages a gibibyte apart: byte offsets beyond 32 bits, in the append too."""
+    m, rng = _m(), np.random.default_rng(14)
+    h, page, d, pages, far = 2, 16, 128, 6, 1 << 30
+    n = page * pages * 4 if new > 90 else page * pages
+    if n > page * pages:                                       # more tokens: the same pages with more slots
+        page *= 4
+    big = [torch.empty((pages - 1) * far + h * page * d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    codes = [b.as_strided((pages, h, page, d // 2), (far, page * d // 2, d // 2, 1)) for b in big]
+    plain = m.NVFP4Cache.empty(pages, h, page, d)
+    cache = m.NVFP4Cache(codes[0], plain.k_scales, plain.k_gscales, codes[1], plain.v_scales, plain.v_gscales)
+    table = _dev(rng.permutation(pages)[None])
+    k, v = (to_dev_bf16(R.bf16(rng, (n, h, d))) for _ in "kv")
+    q = to_dev_bf16(R.bf16(rng, (new, 4 * h, d)))
+    say(f"pages far apart {new}")
+    got = []
+    for c in (cache, plain):
+        m.nvfp4_cache_append(k, v, c, table, _dev([n]), q_offsets=_dev([0, n]))
+        got.append(m.nvfp4_attention(q, c, table, _dev([n]), q_offsets=_dev([0, new])))
+    assert torch.equal(cache.k_codes, plain.k_codes) and torch.equal(cache.v_codes, plain.v_codes)
+    assert torch.equal(got[0], got[1]) and not got[1].isnan().any()

@@ -241,3 +241,24 @@ def test_infinite_and_nan_rows_stay_by_themselves(m_rows, n, k):
     assert torch.equal(got[good], want[good])
     if m_rows > 1:
         assert got[bad].isnan().all()
+
+
+@pytest.mark.parametrize("m_rows,k", [(1, 4096), (5, 4096), (6, 4112)])
+def test_weights_beyond_four_gibibytes(m_rows, k):
+    """The last rows of a large matrix, against the same rows as a matrix of their own."""
+    m, rng = _m(), np.random.default_rng(k)
+    n, tail = 2_099_200, 64
+    w = R.Weight(rng, tail, k)
+    codes = torch.zeros((n, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((n, k // 16), dtype=torch.uint8, device="cuda")
+    codes[-tail:] = torch.from_numpy(w.codes[0]).cuda()
+    scales[-tail:] = torch.from_numpy(w.scales[0]).cuda().view(tail, -1)
+    assert codes.numel() > 1 << 32
+    x = to_dev_bf16(_x(rng, m_rows, k))
+    say(f"large weights {m_rows} {k}")
+    big = m.nvfp4_gemv(x, m.Operand(m.Format.NVFP4, codes, scales, torch.from_numpy(w.S).cuda(), gs=m.GScale.PER_TENSOR),
+                       m_rows, n, k)
+    got = F.bf16_bits_to_f64(from_dev_bf16(big[:, -tail:].contiguous()))
+    ref, tol = R.gemv_ref(F.bf16_bits_to_f64(from_dev_bf16(x)), w.dq[0])
+    _check(got, ref, tol, (m_rows, k))
+    assert (big[:, :-tail] == 0).all()
