@@ -118,7 +118,7 @@ mxq_status nvfp4_cache_append(const uint16_t* k, int64_t k_token_stride, int64_t
  *   lse          NULL, or binary32 [tokens, num_q_heads] contiguous: the natural
  *                log of sum_t exp(x_t)
  *   workspace    device, 16-byte aligned, nvfp4_attention_workspace() bytes (may
- *                be NULL if that is 0); its content before and after means
+ *                be NULL if that is 0; a window may need less); its content before and after means
  *                nothing, calls in flight at once need one each
  * How the context is split follows from the shapes alone (table_width bounds
  * the lengths), so a captured call replays for any lengths, and equal calls

@@ -233,8 +233,11 @@ mxq_status nvfp4_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_
   if ((s = check_rows(fn, "q", q, q_token_stride, q_head_stride, D)) != MXQ_OK) return s;
   if ((s = check_rows(fn, "out", out, out_token_stride, out_head_stride, D)) != MXQ_OK) return s;
   if (!aligned(lse, 4)) return fail(MXQ_EALIGN, "%s: lse 4-byte aligned", fn);
-  const mxq::AttnPlan p = mxq::plan_attention(num_requests, tokens, H, num_q_heads / H, D,
-                                              table_width * cache->page_size, q_offsets != nullptr);
+  a.window = window < I31 ? window : 0;        // positions lie below 2^31: it holds them all
+  // no row sees more than this
+  const int64_t capacity = table_width * cache->page_size;
+  const int64_t reach = a.window && a.window + tokens < capacity ? a.window + tokens : capacity;
+  const mxq::AttnPlan p = mxq::plan_attention(num_requests, tokens, H, num_q_heads / H, D, reach, q_offsets != nullptr);
   if (p.units * H >= I31 / 256 || tokens * num_q_heads >= I31 / 32)      // 32-bit grids
     return fail(MXQ_EUNSUPPORTED, "%s: too many rows for one call", fn);
   const int64_t need = mxq::attention_workspace(p, num_requests, H, D);
@@ -250,7 +253,6 @@ mxq_status nvfp4_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_
   a.Hq = num_q_heads;
   a.G = num_q_heads / H;
   a.scale_log2 = scale * 1.44269504088896340736f;
-  a.window = window < I31 ? window : 0;        // positions lie below 2^31: it holds them all
   a.out = out;
   a.o_token = out_token_stride;
   a.o_head = out_head_stride;

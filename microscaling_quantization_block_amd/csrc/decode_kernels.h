@@ -74,9 +74,14 @@ constexpr int MIN_CHUNK = 8;                   // 32-token tiles of the shortest
 // else six: 64 contexts up to 4096 took 53.8, 56.4, 57.7 us with 512, 768, 1536
 // workgroups aimed at, four contexts up to 131071 110, 104, 93.5.
 constexpr int LONG_CHUNK = 64;
+// No split, and no second launch, where unsplit contexts of at most 2048 tokens
+// give every compute unit a workgroup: 32 contexts up to 1000 tokens, 8 heads
+// 15.6 us, split 19.1; 64 up to 2048 32.1 and 35.3.  From 128 workgroups on: 24
+// up to 2048 (192 workgroups) 24.1 and 21.6.
+constexpr int ENOUGH = 256;
 
-// How a call is cut: column tiles of ct (query, head) pairs, and the number
-// of work units (a bound).
+// How a call is cut (no row sees more than max_context tokens): column tiles
+// of ct (query, head) pairs, and the number of work units (a bound).
 struct AttnPlan {
   int nq, waves, ct, target, coarse;
   int64_t units;
@@ -94,7 +99,8 @@ inline AttnPlan plan_attention(int64_t B, int64_t T, int H, int G, int D, int64_
   // workgroups aimed at
   const int64_t want = p.waves ? 256 : 1536, few = p.waves ? 256 : 512;
   const int64_t most = (max_context + 32 * MIN_CHUNK - 1) / (32 * MIN_CHUNK);   // chunks of the longest context
-  p.target = most <= 2 || tiles * H >= 4 * want ? 0 : (int)((want + H - 1) / H);
+  const bool enough = !p.waves && tiles * H >= ENOUGH && max_context <= 32 * LONG_CHUNK;
+  p.target = most <= 2 || enough || tiles * H >= 4 * want ? 0 : (int)((want + H - 1) / H);
   p.coarse = (int)((few + H - 1) / H);
   const int64_t bound = tiles * most;
   p.units = p.target ? (tiles + p.target < bound ? tiles + p.target : bound) : tiles;

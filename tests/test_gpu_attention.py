@@ -273,3 +273,18 @@ def test_pages_far_apart(new):
         got.append(m.nvfp4_attention(q, c, table, _dev([n]), q_offsets=_dev([0, new])))
     assert torch.equal(cache.k_codes, plain.k_codes) and torch.equal(cache.v_codes, plain.v_codes)
     assert torch.equal(got[0], got[1]) and not got[1].isnan().any()
+
+
+@pytest.mark.parametrize("news", [[1, 1], [3, 2], [150, 60]])
+@pytest.mark.parametrize("d,window", [(64, 100), (128, 700), (256, 300)])
+def test_window_much_shorter_than_the_context(d, window, news):
+    p = Problem(15, d, 1, 2, 16, [3000, 900], news, window=window)
+    p.check(*p.run())
+
+
+def test_many_short_contexts():
+    """More requests than the chip has compute units, none longer than 2048 tokens: not split."""
+    lens = [700, 1, 33, 0] + [40] * 300
+    p = Problem(16, 64, 1, 2, 16, lens, [1] * len(lens))
+    assert _m().nvfp4_attention_workspace(len(lens), 2, 1, 64, 16, p.table.shape[1], len(lens), False) == 0
+    p.check(*p.run(ragged=False))
