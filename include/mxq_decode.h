@@ -84,11 +84,13 @@ typedef struct {
  *               rows there are not stored, and attention does not see them.
  *   seq_lens    [num_requests]: tokens of each request, the new ones included
  *   q_offsets   [num_requests + 1] or NULL: request b has the call's rows
- *               [q_offsets[b], q_offsets[b+1]), non-decreasing; row i of them is
+ *               [q_offsets[b], q_offsets[b+1]), non-decreasing, within
+ *               [0, tokens]; row i of them is
  *               position seq_lens[b] - (their number) + i.  NULL: one row per
  *               request (tokens == num_requests).  Rows before q_offsets[0] or
- *               from the last offset on belong to no request: nothing is read
- *               or written for them.
+ *               from the last offset on belong to no request, and a request
+ *               whose offsets leave [0, tokens] has no rows: nothing is read
+ *               or written for either.
  *
  * nvfp4_cache_append -- quantizes the call's K and V rows into the cache.
  *   k, v             BF16 [tokens, num_heads, head_dim], strides in elements

@@ -259,6 +259,7 @@ mxq_status nvfp4_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_
   a.lse = lse;
   a.target = p.target;
   a.coarse = p.coarse;
+  a.units = p.units;
   if (need) {
     const int64_t rows = p.units * H * p.ct;
     a.part_o = static_cast<float*>(workspace);

@@ -156,13 +156,9 @@ __device__ __forceinline__ RequestSize request_size(const AttnArgs& a, int64_t b
   RequestSize r = {0, 0, 0, 0, 0};
   if (b >= cc.B) return r;
   r.L = max(cc.seq_lens[b], 0);
-  r.q_begin = (int)b;
-  r.q_len = 1;
-  if (cc.q_offsets) {
-    r.q_begin = cc.q_offsets[b];
-    const int end = cc.q_offsets[b + 1];
-    r.q_len = r.q_begin >= 0 && end <= a.T && end > r.q_begin ? end - r.q_begin : 0;
-  }
+  const RequestRows rows = request_rows(cc, b, a.T);
+  r.q_begin = rows.begin;
+  r.q_len = rows.len;
   r.cts = (int)(((int64_t)r.q_len * a.G + CT - 1) / CT);
   int64_t n = (int64_t)cc.width << cc.P_log2;
   n = n < r.L ? n : r.L;
@@ -1112,7 +1108,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int CT)
   const int64_t row = ((int64_t)blockIdx.x * 4 + wave) / RW, rows = a.T * a.Hq;
   if (row >= rows) return;
   const int64_t tq = row / a.Hq, head = row - tq * a.Hq;
-  const int64_t b = request_of(a.c, tq);
+  const int64_t b = request_of(a.c, tq, a.T);
   if (b < 0) return;                           // a row of no request is left as it was
   const int2 ix = a.part_index[b];
   const int chunks = ix.y;
@@ -1120,7 +1116,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int CT)
   const int h = (int)(head / a.G);
   const int64_t j = (tq - (a.c.q_offsets ? a.c.q_offsets[b] : tq)) * a.G + (head - (int64_t)h * a.G);
   const int64_t stride = (int64_t)a.c.H * CT;  // of a chunk
-  const int64_t first = (((int64_t)ix.x + j / CT * chunks) * a.c.H + h) * CT + j % CT;
+  const int64_t unit = ix.x + j / CT * chunks;  // of chunk 0
+  if (unit < 0 || unit + chunks > a.units) return;   // offsets out of order name more units than the grid has
+  const int64_t first = (unit * a.c.H + h) * CT + j % CT;
   float mx = NEG_INF;
   for (int k = lane; k < chunks; k += 64) mx = fmaxf(mx, a.part_lse[first + k * stride]);
 #pragma unroll

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
   const int64_t h = is_v ? hv - c.H : hv;
   const uint16_t* src = is_v ? a.v + t * a.v_token + h * a.v_head : a.k + t * a.k_token + h * a.k_head;
   const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * lane);
-  const int64_t b = request_of(c, t);
+  const int64_t b = request_of(c, t, a.T);
   if (b < 0) return;
   const int64_t q_end = c.q_offsets ? c.q_offsets[b + 1] : t + 1;
   const int64_t pos = c.seq_lens[b] - q_end + t;

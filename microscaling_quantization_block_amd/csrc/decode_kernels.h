@@ -66,6 +66,7 @@ struct AttnArgs {
   // chunks of all requests: at most `target` beside one per column tile, `coarse` if that
   // makes none longer than LONG_CHUNK; target 0: a request's context is one chunk
   int target, coarse;
+  int64_t units;                // of the grid (times the KV heads)
 };
 
 constexpr int MANY_WAVES = 8;                  // waves of a workgroup with many columns
