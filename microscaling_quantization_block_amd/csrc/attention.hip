@@ -402,9 +402,11 @@ __device__ __forceinline__ void store_run(const AttnArgs& a, const Unit& u, int6
   for (int d = 0; d < N; d += 2) *reinterpret_cast<uint32_t*>(out + d) = f32x2_to_bf16x2(v[d], v[d + 1]);
 }
 // The log sum of a column; m: its maximum as a logit (log2), l: its sum
-// against 2^(BASE - m).
+// against 2^(BASE - m).  The sum is 0 exactly where nothing is in reach (the
+// largest exponential is 2^BASE at least), and NaN where a logit is NaN: that
+// stays NaN here, in the row and through the join.
 __device__ __forceinline__ void store_lse(const AttnArgs& a, const Unit& u, int64_t pr, int64_t row, float m, float l) {
-  const float lse2 = l > 0.0f ? m - BASE + __builtin_amdgcn_logf(l) : NEG_INF;   // log2
+  const float lse2 = l == 0.0f ? NEG_INF : m - BASE + __builtin_amdgcn_logf(l);  // log2
   if (u.chunks > 1) a.part_lse[pr] = lse2;
   else if (a.lse) a.lse[row] = lse2 * 0.693147180559945309f;
 }
@@ -742,7 +744,7 @@ __global__ __launch_bounds__(256, D <= 128 && NQ == 1 ? 3 : 2) void attention_fe
     float lt = 0.0f;
 #pragma unroll
     for (int w = 0; w < FEW_WAVES; ++w) lt += __builtin_amdgcn_exp2f(mw[w] - top) * lw[w];
-    const float f = lt > 0.0f ? __builtin_ldexpf(__builtin_amdgcn_exp2f(m[n] - top) / lt, o.e_ref) : 0.0f;
+    const float f = lt == 0.0f ? 0.0f : __builtin_ldexpf(__builtin_amdgcn_exp2f(m[n] - top) / lt, o.e_ref);
     m[n] = mx;
     l[n] = lt;
 #pragma unroll
@@ -1082,7 +1084,7 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
     const auto sw = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
     l = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
   }
-  const float f = l > 0.0f ? __builtin_ldexpf(1.0f / l, e_ref - 4) : 0.0f;
+  const float f = l == 0.0f ? 0.0f : __builtin_ldexpf(1.0f / l, e_ref - 4);
   store_index(a, u, h);
   if (!have) return;
   const int64_t pr = ((int64_t)uid * cc.H + h) * Y::CT + wave * 32 + c;
@@ -1097,7 +1099,9 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
   }
 }
 
-// Joins the chunks of one (token, head): weights 2^(lse_s - lse).  RW waves
+// Joins the chunks of one (token, head): weights 2^(lse_s - lse).  Every chunk
+// has written its row, an empty one zeros; a NaN in a chunk's sum or row reaches
+// the output.  RW waves
 // share a row's chunks (and meet in LDS): four where there are few rows, whose
 // contexts are cut into many chunks then; eight chunks' rows are in flight.
 template <int D, int RW>
@@ -1143,7 +1147,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int CT)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int q = 0; q < DL; ++q) o[q] += wk[i] > 0.0f ? wk[i] * v[i][q] : 0.0f;   // an empty chunk wrote no row
+        for (int q = 0; q < DL; ++q) o[q] += k + i * RW < n ? wk[i] * v[i][q] : 0.0f;
     }
   }
 #pragma unroll
@@ -1157,12 +1161,12 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int CT)
     for (int q = 0; q < DL; ++q)
       for (int i = 1; i < RW; ++i) o[q] += s_o[((wave + i) * DL + q) * 64 + lane];
   }
-  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   uint16_t* out = a.out + tq * a.o_token + head * a.o_head + lane * DL;
 #pragma unroll
   for (int q = 0; q < DL; ++q) out[q] = (uint16_t)f32x2_to_bf16x2(o[q] * inv, 0.0f);
   if (a.lse && lane == 0)
-    a.lse[row] = total > 0.0f ? (mx + __builtin_amdgcn_logf(total)) * 0.693147180559945309f : NEG_INF;
+    a.lse[row] = total == 0.0f ? NEG_INF : (mx + __builtin_amdgcn_logf(total)) * 0.693147180559945309f;
 }
 
 template <int D, int NQ>

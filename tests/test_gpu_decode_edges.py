@@ -49,3 +49,68 @@ def test_offsets_outside_the_call(lens, split, offs, none):
     changed = (cache.k_codes != before[0]).any(-1)
     assert changed.sum() == (1 if none else 2)
     assert not torch.equal(cache.v_gscales, before[1])
+
+
+# few columns unsplit, split; many columns unsplit, split; many columns with one KV head per query head
+SHAPES = [([40, 33], [3, 2], 4), ([3000, 40], [1, 1], 4), ([300, 90], [1, 70], 4), ([3000], [150], 4), ([700], [600], 1)]
+
+
+def _shape(seed, lens, news, grp, d=128, **kw):
+    p = Problem(seed, d, 1, grp, 16, lens, news, **kw)
+    return p, p.cache.device(_m(), torch)
+
+
+def _call(p, cache, q=None):
+    say(f"lens {p.lens} new {p.news} window {p.window} grp {p.grp} d {p.d}")
+    return _m().nvfp4_attention(to_dev_bf16(p.q) if q is None else q, cache, _dev(p.table), _dev(p.lens),
+                                q_offsets=_dev(p.offs), scale=p.scale, window=p.window, with_lse=True)
+
+
+def _place(p, t, b=0):
+    """Page and slot of token t of request b."""
+    return int(p.table[b, t // p.page]), t % p.page
+
+
+def _sees(p, t, b=0):
+    """Which rows of the call have token t of request b in reach."""
+    rows = torch.zeros(p.total, dtype=torch.bool, device="cuda")
+    for i in range(p.news[b]):
+        pos = p.lens[b] - p.news[b] + i
+        rows[p.offs[b] + i] = t <= pos and (not p.window or t > pos - p.window)
+    return rows
+
+
+def _check_others(p, sees, out, lse, want, want_lse):
+    """The rows that do not see the spoilt token are within their bounds (the others replaced by the clean call's)."""
+    pick = sees[:, None]
+    p.check(torch.where(pick[..., None], want, out), torch.where(pick, want_lse, lse))
+
+
+@pytest.mark.parametrize("lens,news,grp", SHAPES)
+@pytest.mark.parametrize("bad", [float("nan")])
+def test_a_spoilt_query_row_is_nan(lens, news, grp, bad):
+    """An infinity or a NaN in a row and head makes its output and its log sum NaN, however the context is cut."""
+    p, cache = _shape(21, lens, news, grp)
+    q = to_dev_bf16(p.q)
+    row, head = 0, grp - 1
+    q[row, head, 7] = bad
+    out, lse = _call(p, cache, q)
+    assert out[row, head].isnan().all() and lse[row, head].isnan()
+    out[row, head], lse[row, head] = 0.0, 0.0
+    assert out.isfinite().all() and lse.isfinite().all()
+
+
+@pytest.mark.parametrize("lens,news,grp", SHAPES)
+def test_a_spoilt_key_is_nan_where_it_is_seen(lens, news, grp):
+    """A key whose second scale is NaN: the rows that reach it are NaN, log sum too; the others stand."""
+    p, cache = _shape(22, lens, news, grp)
+    want, want_lse = _call(p, cache)
+    for t in {5, lens[0] - (news[0] + 1) // 2}:
+        page, slot = _place(p, t)
+        keep = cache.k_gscales[page, 0, slot].clone()
+        cache.k_gscales[page, 0, slot] = float("nan")
+        out, lse = _call(p, cache)
+        cache.k_gscales[page, 0, slot] = keep
+        sees = _sees(p, t)
+        assert sees.any() and out[sees].isnan().all() and lse[sees].isnan().all(), t
+        _check_others(p, sees, out, lse, want, want_lse)
