@@ -255,12 +255,14 @@ __device__ __forceinline__ int2 chunk_tiles(const Unit& u, const Reach& r) {
 // A query row in FP16: its elements times 2^e, the largest then in [2^13, 2^14).
 // cs is the factor of a logit (log2) per unit of that product.  It is kept
 // positive (maxima are taken before it is applied): its sign goes to q, and
-// where it vanishes, q does.
+// where it vanishes, q does.  A row with an infinity or a NaN becomes all NaN:
+// logits of -infinity would look like tokens out of reach.
 __device__ __forceinline__ int query_exponent(uint32_t amax, float scale_log2, float& cs, float& sign) {
   const int e = amax ? 13 - ((int)(amax >> 7) - 127) : 0;
   cs = __builtin_ldexpf(fabsf(scale_log2), -e);
   sign = scale_log2 < 0.0f ? -1.0f : 1.0f;
   if (!(cs > 0.0f)) cs = 1.0f, sign = 0.0f;
+  if (amax >= 0x7F80u) sign = __builtin_nanf("");
   return e;
 }
 __device__ __forceinline__ f16x8 query_fragment(uint4 w, int e, float sign) {

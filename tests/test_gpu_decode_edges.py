@@ -87,13 +87,16 @@ def _check_others(p, sees, out, lse, want, want_lse):
 
 
 @pytest.mark.parametrize("lens,news,grp", SHAPES)
-@pytest.mark.parametrize("bad", [float("nan")])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_a_spoilt_query_row_is_nan(lens, news, grp, bad):
     """An infinity or a NaN in a row and head makes its output and its log sum NaN, however the context is cut."""
     p, cache = _shape(21, lens, news, grp)
     q = to_dev_bf16(p.q)
     row, head = 0, grp - 1
     q[row, head, 7] = bad
+    # every key has the same sign there: infinite logits of one sign, no NaN among them
+    p.cache.t["k_codes"][..., 3] = (p.cache.t["k_codes"][..., 3] & 0x0F) | 0x20
+    cache = p.cache.device(_m(), torch)
     out, lse = _call(p, cache, q)
     assert out[row, head].isnan().all() and lse[row, head].isnan()
     out[row, head], lse[row, head] = 0.0, 0.0
