@@ -99,7 +99,8 @@ typedef struct {
  *                    the values stored, bf16(fl(fl(c s_b) S)) as mx_dequantize
  *                    gives them (written also for a row without a page)
  * Two rows of one call that land on the same slot leave either of them there,
- * or a mixture.
+ * or a mixture.  A row with an infinity or a NaN is stored with a NaN second
+ * scale, so that all its values are NaN.
  */
 mxq_status nvfp4_cache_append(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
                               int64_t v_token_stride, int64_t v_head_stride, int64_t tokens, const mxq_cache* cache,

@@ -3,7 +3,11 @@
 // A row is the D values of one token and KV head.  It is quantized exactly as
 // nvfp4_quantize does a row under a per-row second scale (nearest even):
 // S = fl(amax / 2688), s_b = E4M3(fl(a_b / fl(6 S))), codes E2M1 of
-// fl(x fl(1 / fl(s_b S))).  D / 8 lanes hold a row, eight values each (one
+// fl(x fl(1 / fl(s_b S))).  One with an infinity or a NaN gets a NaN for S:
+// every value of it is NaN then, and the attention meets no infinite second scale,
+// whose logits might be -infinity and look like tokens out of reach.
+//
+// D / 8 lanes hold a row, eight values each (one
 // 16-byte load), a block is a lane pair; the row maximum is an integer
 // maximum over the lanes.  A decode step (128 rows of 8 heads, 3.6 us) is one
 // chain of latencies: request, offsets, page, store.  A prompt (10 k tokens of 8 heads)
@@ -48,7 +52,8 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
   uint32_t amax = a_b;
 #pragma unroll
   for (int s = 2; s < L; s *= 2) amax = umax(amax, lane_xor_u32(amax, s));
-  const float S = __uint_as_float(amax) / 2688.0f;
+  // a row with an infinity or a NaN: all its values are NaN
+  const float S = amax < 0x7F800000u ? __uint_as_float(amax) / 2688.0f : __builtin_nanf("");
   const BlockScale bs = nv_block_scale(__uint_as_float(a_b), S);
   const u32x4 none = {0, 0, 0, 0};
   const uint32_t code = S < TINY_S ? nv_encode8<false, true>(x, bs.r, none) : nv_encode8<false, false>(x, bs.r, none);

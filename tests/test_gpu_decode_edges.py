@@ -117,3 +117,25 @@ def test_a_spoilt_key_is_nan_where_it_is_seen(lens, news, grp):
         sees = _sees(p, t)
         assert sees.any() and out[sees].isnan().all() and lse[sees].isnan().all(), t
         _check_others(p, sees, out, lse, want, want_lse)
+
+
+@pytest.mark.parametrize("lens,news,grp", SHAPES)
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_an_infinite_row_is_stored_as_nan(lens, news, grp, bad, which):
+    """A K or V row with an infinity or a NaN has a NaN second scale: its values are NaN, and so is what sees it."""
+    m = _m()
+    p, cache = _shape(23, lens, news, grp)
+    t = lens[0] - news[0]                                     # the first new token: every new row sees it
+    page, slot = _place(p, t)
+    rows = {n: torch.ones((1, 1, 128), dtype=torch.bfloat16, device="cuda") for n in "kv"}
+    rows[which][0, 0, 77] = bad
+    say(f"appended {which} {bad}")
+    kd, vd = m.nvfp4_cache_append(rows["k"], rows["v"], cache, _dev(p.table[:1]), _dev([t + 1]), with_dq=True)
+    S = cache.k_gscales if which == "k" else cache.v_gscales
+    assert S[page, 0, slot].isnan() and (kd if which == "k" else vd).isnan().all()
+    assert (vd if which == "k" else kd).isfinite().all()
+    out, lse = _call(p, cache)
+    rows = slice(p.offs[0], p.offs[1])
+    assert out[rows].isnan().all() and not out[p.offs[1]:].isnan().any()
+    assert lse[rows].isnan().all() if which == "k" else lse.isfinite().all()
