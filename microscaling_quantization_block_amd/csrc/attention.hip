@@ -15,6 +15,14 @@
 // to FP16, 2^-11 relative.  Sums, maxima and logits are binary32, and l sums
 // the exponentials before they are rounded.
 //
+// What a column does not reach must not count, whatever it holds.  Its logit is
+// replaced by -infinity; but V's values are shared by the columns of a tile, and
+// 0 times NaN is NaN.  On border tiles, which hold tokens that some columns reach
+// and others do not, S_t therefore goes to the weights of the columns that reach
+// t, Sref is each column's own (a token 2^25 times larger than the others would
+// push the weights of the rows before it out of FP16), and a NaN among a token's
+// block scales is taken out of the shared values and put into S_t.
+//
 // Orientation: logits are computed transposed, X^T = K Q^T (A = tokens, B = query
 // columns), and the output too, O^T = V^T W^T.  A lane then holds one column in
 // both, so the softmax statistics and every rescaling are lane-local but for
@@ -289,7 +297,7 @@ struct Columns {
   // a logit exceeds it by HEADROOM (log2), i.e. when q . k > limit.
   // mu = BASE - m cs
   float m[NQ], mu[NQ], limit[NQ];
-  int e_ref;                    // Sref = 2^e_ref
+  int e_ref[NQ];                // Sref = 2^e_ref
 };
 
 template <int D, int NQ>
@@ -325,40 +333,33 @@ __device__ __forceinline__ void load_columns(const AttnArgs& a, const Unit& u, i
     o.m[n] = NEG_INF;
     o.limit[n] = NEG_INF;
     o.mu[n] = BASE;
+    o.e_ref[n] = -100;
 #pragma unroll
     for (int d = 0; d < ND; ++d) o.acc[n][d] = f32x4{0, 0, 0, 0};
   }
-  o.e_ref = -100;
 }
 
-// Masks the logits of a border tile.
+// A border tile's logits and second scales of V as column n sees them.
 template <int D, int NQ>
-__device__ __forceinline__ void mask_logits(const Columns<D, NQ>& o, int n, f32x4* x, const TilePages& tp, int tile,
-                                            int g) {
+__device__ __forceinline__ void mask_column(const Columns<D, NQ>& o, int n, f32x4* x, f32x4* vg, const TilePages& tp,
+                                            int tile, int g) {
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int t0 = tile * TILE + 16 * s + 4 * g;
     const int last = tp.p[s] < 0 ? -1 : o.pos[n];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[s][i] = (t0 + i <= last) & (t0 + i > o.lo[n]) ? x[s][i] : NEG_INF;
+    for (int i = 0; i < 4; ++i) {
+      const bool sees = (t0 + i <= last) & (t0 + i > o.lo[n]);
+      x[s][i] = sees ? x[s][i] : NEG_INF;
+      vg[s][i] = sees ? vg[s][i] : 0.0f;
+    }
   }
 }
 
-// A token outside [begin, end), or without a page, may hold any bytes: its V
-// scales become zero (and its logit -inf).
-__device__ __forceinline__ void drop_unused(f32x4* vg, uint32_t* vs, const TilePages& tp, int tile, int begin, int end,
-                                            int g) {
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int t0 = tile * TILE + 16 * s + 4 * g;
-    const int stop = tp.p[s] < 0 ? -1 : end;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool use = (t0 + i >= begin) & (t0 + i < stop);
-      vg[s][i] = use ? vg[s][i] : 0.0f;
-      vs[s] &= use ? 0xFFFFFFFFu : ~(0xFFu << (8 * i));
-    }
-  }
+// 0xFF in the bytes that are NaN as E4M3 numbers.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  const uint32_t m = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return m | (m - (m >> 7));
 }
 
 // Moves the maxima that a tile's logits x exceed by more than the headroom;
@@ -543,10 +544,21 @@ __device__ __forceinline__ void read_tile(const uint8_t* raw, int c, int g, RawT
 // One tile.  `inside`: every token is in reach of every column.
 template <int D, int NQ>
 __device__ __forceinline__ void attend_tile(Columns<D, NQ>& o, float* l, RawTile<D>& r, const TilePages& tp, int tile,
-                                            int t_begin, int t_end, bool inside, int c, int g) {
+                                            bool inside, int c, int g) {
   constexpr int KF = D / 32, ND = D / 16;
   if (!inside) {
-    drop_unused(r.vg, r.vs, tp, tile, t_begin, t_end, g);
+    // NaN block scales: the 16 lanes of a group hold the blocks of the same four tokens
+    const uint32_t nan[2] = {nan_bytes(r.vs[0]), nan_bytes(r.vs[1])};
+    if (__any((nan[0] | nan[1]) != 0))
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        r.vs[s] &= ~nan[s];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t hit = __ballot((nan[s] >> (8 * i) & 1) != 0);
+          if (hit >> (16 * g) & 0xFFFF) r.vg[s][i] = __builtin_nanf("");
+        }
+      }
   }
   // logits
   f32x4 x[NQ][2];
@@ -563,25 +575,39 @@ __device__ __forceinline__ void attend_tile(Columns<D, NQ>& o, float* l, RawTile
       for (int n = 0; n < NQ; ++n) x[n][s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, o.q[n][j], x[n][s], 0, 0, 0);
     }
   }
-  // Sref: a power of two above every second scale of V seen so far
-  float smax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) smax = fmaxf(smax, fmaxf(r.vg[0][i], r.vg[1][i]));
-  smax = max_groups(smax);
-  const int e_tile = __builtin_amdgcn_readfirstlane((int)(__float_as_uint(smax) >> 23) - 126);
-  if (e_tile > o.e_ref) {
-    const float grow = __builtin_ldexpf(1.0f, o.e_ref - e_tile);
-    o.e_ref = e_tile;
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-      for (int d = 0; d < ND; ++d) o.acc[n][d] *= grow;
-  }
+  f32x4 f[NQ][2];                              // the second scales of V, over Sref further down
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) x[n][s] *= r.kg[s];
-    if (!inside) mask_logits(o, n, x[n], tp, tile, g);
+    for (int s = 0; s < 2; ++s) {
+      x[n][s] *= r.kg[s];
+      f[n][s] = r.vg[s];
+    }
+    if (!inside) mask_column(o, n, x[n], f[n], tp, tile, g);
+  }
+  // Sref: a power of two above every second scale of V that the column has seen so far
+  int e_tile[NQ];
+  bool grows = false;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    if (n > 0) e_tile[n] = e_tile[0];          // inside, all columns see the same tokens
+    if (n == 0 || !inside) {
+      float smax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) smax = fmaxf(smax, fmaxf(f[n][0][i], f[n][1][i]));
+      e_tile[n] = (int)(__float_as_uint(max_groups(smax)) >> 23) - 126;
+    }
+    grows = grows || e_tile[n] > o.e_ref[n];
+  }
+  if (__any(grows)) {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int e = max(o.e_ref[n], e_tile[n]);
+      const float grow = __builtin_ldexpf(1.0f, o.e_ref[n] - e);
+      o.e_ref[n] = e;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o.acc[n][d] *= grow;
+    }
   }
   float alpha[NQ];
   if (move_maxima(o, x, alpha))
@@ -591,11 +617,6 @@ __device__ __forceinline__ void attend_tile(Columns<D, NQ>& o, float* l, RawTile
 #pragma unroll
       for (int d = 0; d < ND; ++d) o.acc[n][d] *= alpha[n];
     }
-  f32x4 f[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[s][i] = __builtin_ldexpf(r.vg[s][i], -o.e_ref);
   f16x8 wf[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
@@ -605,7 +626,7 @@ __device__ __forceinline__ void attend_tile(Columns<D, NQ>& o, float* l, RawTile
       for (int i = 0; i < 4; ++i) {
         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][s][i], o.cs[n], o.mu[n]));
         l[n] += p;                             // of this lane group's tokens
-        x[n][s][i] = p * f[s][i];
+        x[n][s][i] = p * __builtin_ldexpf(f[n][s][i], -o.e_ref[n]);
       }
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
@@ -711,7 +732,7 @@ __global__ __launch_bounds__(256, D <= 128 && NQ == 1 ? 3 : 2) void attention_fe
       now.p[0] = ok & 1 ? 0 : -1;
       now.p[1] = ok & 2 ? 0 : -1;
       const bool inside = (tile * TILE >= re.all_begin) & ((tile + 1) * TILE <= re.all_end) & ((ok & 3) == 3);
-      attend_tile<D, NQ>(o, l, r, now, tile, re.begin, re.end, inside, c, g);
+      attend_tile<D, NQ>(o, l, r, now, tile, inside, c, g);
       ok >>= 2;
       slot = slot == FEW_AHEAD ? 0 : slot + 1;
     }
@@ -746,7 +767,7 @@ __global__ __launch_bounds__(256, D <= 128 && NQ == 1 ? 3 : 2) void attention_fe
     float lt = 0.0f;
 #pragma unroll
     for (int w = 0; w < FEW_WAVES; ++w) lt += __builtin_amdgcn_exp2f(mw[w] - top) * lw[w];
-    const float f = lt == 0.0f ? 0.0f : __builtin_ldexpf(__builtin_amdgcn_exp2f(m[n] - top) / lt, o.e_ref);
+    const float f = lt == 0.0f ? 0.0f : __builtin_ldexpf(__builtin_amdgcn_exp2f(m[n] - top) / lt, o.e_ref[n]);
     m[n] = mx;
     l[n] = lt;
 #pragma unroll
@@ -801,6 +822,11 @@ __global__ __launch_bounds__(256, D <= 128 && NQ == 1 ? 3 : 2) void attention_fe
 // 16 kk + 8 + 4 hh + i (i < 4), kk = 0, 1.  V carries its second scale here, V' =
 // fp16(c fp16(s_b S_t 2^4 / Sref)), so that the weights are the plain
 // exponentials.
+//
+// That holds for the whole tiles, whose tokens all columns of the workgroup
+// reach.  The others, the border tiles, have fragments of c s_b 2^4 (exact), and
+// S_t goes to the weights (a second rounding of those), over a Sref of the column,
+// 2^bump times the shared one.
 template <int D>
 struct ManyLayout {
   static constexpr int W = MANY_WAVES, CT = 32 * W;
@@ -835,6 +861,10 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
   const Reach wg = reach(a, u, col_wg, col_wg + Y::CT), re = reach(a, u, col0, col0 + 32);
   const int2 tiles = chunk_tiles(u, wg);
   const int count = tiles.y - tiles.x;
+  const int w0 = (wg.all_begin + TILE - 1) / TILE, w1 = wg.all_end / TILE;   // the whole tiles
+  auto is_whole = [&](int tile, int valid) { return (tile >= w0) & (tile < w1) & (valid == 3); };
+  // phases of whole tiles only, but for missing pages
+  const int pw0 = (max(w0 - tiles.x, 0) + PH - 1) / PH, pw1 = (min(w1, tiles.y) - tiles.x) / PH;
 
   // loads: phase p into ring slot p % RING
   // (a wave without a load of its own repeats the last one, the same bytes to
@@ -857,7 +887,7 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
     for (int i = 0; i < PH; ++i) {
       const int tile = tiles.x + p * PH + i;
       TilePages tp = pages[i];
-      if (tile >= tiles.y) tp.p[0] = tp.p[1] = -1;              // keeps the number of loads in flight
+      if (p * PH + i >= count) tp.p[0] = tp.p[1] = -1;          // keeps the number of loads in flight
       ok |= (uint32_t)((tp.p[0] >= 0) | (tp.p[1] >= 0) << 1) << (2 * (ahead * PH + i));
       const int p0 = max(tp.p[0], 0), p1 = max(tp.p[1], 0);
       const int s0 = (tile * TILE) & page_mask, s1 = (tile * TILE + 16) & page_mask;
@@ -907,32 +937,50 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
   for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
   float m = NEG_INF, limit = NEG_INF, mu = BASE, l = 0.0f;
   int e_ref = -100, e_fill = -100;             // exponents of Sref: of the sums, of the fragments made last
+  int bump = 0;                                // the column's sums are on 2^(e_ref + bump)
+  bool bumped = false, apart = false;          // a column of the wave has a bump; has one and meets whole tiles
+  bool whole_now = false, whole_next = false;  // this phase, the next one: whole tiles only
 
-  // ranges of tiles of the chunk: some token in reach of the wave's columns, every
-  // token in reach of all of them, every token inside the workgroup's range
-  const int any0 = re.begin / TILE - tiles.x, any1 = (re.end + TILE - 1) / TILE - tiles.x;
-  const int all0 = (re.all_begin + TILE - 1) / TILE - tiles.x, all1 = re.all_end / TILE - tiles.x;
-  const int in0 = (wg.begin + TILE - 1) / TILE - tiles.x, in1 = wg.end / TILE - tiles.x;
+  // ranges of tiles: some token in reach of the wave's columns, every token in reach of all of them
+  const int any0 = re.begin / TILE, any1 = (re.end + TILE - 1) / TILE;
+  const int all0 = (re.all_begin + TILE - 1) / TILE, all1 = re.all_end / TILE;
 
   // The exponent of Sref for phase p, whose tiles are there: a power of two
-  // above every second scale of V so far.
+  // above every second scale of V in the whole tiles so far.  In a border tile, a
+  // token with a NaN among its block scales gets a NaN for S: the fragments go
+  // without the NaN (all waves write the same, for attend alone).
   auto scale_of = [&](int p, int shift) {
-    const int i = PH == 2 ? hh : 0, n = p * PH + i, valid = (int)(ok >> (2 * (shift * PH + i))) & 3;
-    float v = reinterpret_cast<const float*>(s_many + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW + Y::VG)[c];
-    const int t = (tiles.x + n) * TILE + c;
-    v = (t >= wg.begin) & (t < wg.end) & (valid >> (c >> 4) & 1) ? v : 0.0f;
+    constexpr uint32_t ALL = (1u << (2 * PH)) - 1;
+    whole_next = (p >= pw0) & (p < pw1) & ((ok >> (2 * PH * shift) & ALL) == ALL);
+    const int h2 = PH == 2 ? hh : 0;
+    float v = reinterpret_cast<const float*>(s_many + Y::RAW0 + ((p & (Y::RING - 1)) * PH + h2) * Y::RAW + Y::VG)[c];
+    if (__builtin_expect(!whole_next, 0)) {
+#pragma unroll
+      for (int i = 0; i < PH; ++i) {
+        if (is_whole(tiles.x + p * PH + i, (int)(ok >> (2 * (shift * PH + i))) & 3)) continue;
+        if (PH == 1 || hh == i) v = 0.0f;
+        uint8_t* raw = s_many + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW;
+#pragma unroll
+        for (int w = 0; w < (D + 127) / 128; ++w) {
+          const int at = (64 * w + lane) & (D / 2 - 1);         // word: block at / 8, tokens 4 (at % 8) ..
+          const uint32_t nan = nan_bytes(*reinterpret_cast<const uint32_t*>(raw + Y::VS + 4 * at));
+          if (nan)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              if (nan >> (8 * t) & 1) reinterpret_cast<float*>(raw + Y::VG)[4 * (at & 7) + t] = __builtin_nanf("");
+        }
+      }
+    }
     e_fill = max(e_fill, (int)(wave_max_u32(__float_as_uint(v)) >> 23) - 126);
   };
 
-  // Makes the fragments of tile i of phase p.  A token outside the range, or
-  // without a page, may hold any bytes: its V scales count as zero (and its
-  // logit as -inf).
+  // Makes the fragments of tile i of phase p.
   auto fill = [&](int p, int i, int shift) {
-    const int n = p * PH + i, tile = tiles.x + n, valid = (int)(ok >> (2 * (shift * PH + i))) & 3;
+    const int tile = tiles.x + p * PH + i, valid = (int)(ok >> (2 * (shift * PH + i))) & 3;
     const uint8_t* raw = s_many + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW;
     uint4* frag = reinterpret_cast<uint4*>(s_many) + ((p & 1) * PH + i) * F * 64 + lane;
-    const bool inside = (n >= in0) & (n < in1) & (valid == 3);
-    const float to_ref = __builtin_ldexpf(1.0f, 4 - e_fill);
+    const bool whole = whole_next || is_whole(tile, valid);
+    const float to_ref = __builtin_ldexpf(1.0f, whole ? 4 - e_fill : 4);
     // K: fragment j holds the values hh D / 2 + 8 j of token c
     const int kfirst = NK >= W ? wave : wave % NK;
     if (NK >= W || wave < NK)
@@ -956,19 +1004,15 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
           const int r = 16 * kk + 8 * b + 4 * hh;
           f32x4 vg = *reinterpret_cast<const f32x4*>(raw + Y::VG + 4 * r);
           uint32_t vs = *reinterpret_cast<const uint32_t*>(raw + Y::VS + (c * DT / 16) * 32 + r);
-          if (!inside)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const int at = tile * TILE + r + t;
-              const bool use = (at >= wg.begin) & (at < wg.end) & ((valid >> kk) & 1);
-              vg[t] = use ? vg[t] : 0.0f;
-              vs &= use ? 0xFFFFFFFFu : ~(0xFFu << (8 * t));
-            }
+          if (__builtin_expect(!whole, 0)) {
+            vg = f32x4{1, 1, 1, 1};
+            vs &= ~nan_bytes(vs);
+          }
           uint32_t w[4];
 #pragma unroll
           for (int t = 0; t < 4; ++t)
             w[t] = (*reinterpret_cast<const uint32_t*>(codes + v_row(r + t) * (D / 2)) >> sh) & 15u;
-          // the conversion applies the power of two
+          // the conversion applies the power of two; the factor of a border tile is exact
           const mxq_f32x2 b0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(vs, to_ref, false);
           const mxq_f32x2 b1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(vs, to_ref, true);
           const mxq_f32x2 f0 = {b0.x * vg[0], b0.y * vg[1]}, f1 = {b1.x * vg[2], b1.y * vg[3]};
@@ -981,8 +1025,8 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
   };
 
   auto attend = [&](int p, int i) {
-    const int n = p * PH + i, tile = tiles.x + n, valid = (int)(ok >> (2 * i)) & 3;
-    if ((n < any0) | (n >= any1) | (n >= count)) return;
+    const int tile = tiles.x + p * PH + i, valid = (int)(ok >> (2 * i)) & 3;
+    if ((tile < any0) | (tile >= any1) | (p * PH + i >= count)) return;
     const uint4* frag = reinterpret_cast<const uint4*>(s_many) + ((p & 1) * PH + i) * F * 64 + lane;
     const uint8_t* raw = s_many + Y::RAW0 + ((p & (Y::RING - 1)) * PH + i) * Y::RAW;
     // fragments are read eight at a time, V's first ones before the
@@ -1007,13 +1051,14 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
     // element i of x: token 8 (i / 4) + 4 hh + i % 4
 #pragma unroll
     for (int i2 = 0; i2 < 16; ++i2) x[i2] *= kg[i2 >> 2][i2 & 3];
-    if ((n < all0) | (n >= all1) | (valid != 3)) {
+    auto sees = [&](int i2) {
+      const int t = tile * TILE + 8 * (i2 >> 2) + 4 * hh + (i2 & 3);
+      return (t <= ((valid >> (i2 >> 3)) & 1 ? pos : -1)) & (t > lo);
+    };
+    const bool masked = (tile < all0) | (tile >= all1) | (valid != 3);
+    if (__builtin_expect(!whole_now, 0) && masked) {
 #pragma unroll
-      for (int i2 = 0; i2 < 16; ++i2) {
-        const int t = tile * TILE + 8 * (i2 >> 2) + 4 * hh + (i2 & 3);
-        const int last = (valid >> (i2 >> 3)) & 1 ? pos : -1;
-        x[i2] = (t <= last) & (t > lo) ? x[i2] : NEG_INF;
-      }
+      for (int i2 = 0; i2 < 16; ++i2) x[i2] = sees(i2) ? x[i2] : NEG_INF;
     }
     float mx = x[0];
 #pragma unroll
@@ -1041,6 +1086,46 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
       wf[i2 >> 3][i2 & 7] = hp.x;
       wf[i2 >> 3][(i2 & 7) + 1] = hp.y;
     }
+    // The weights of a border tile, and those of columns with a bump.  (Out of line,
+    // and without a second copy of the products: with one the compiler moves the
+    // sums about, 968 us for the prompt chunks against 793.)
+    if (__builtin_expect(!whole_now | apart, 0)) {
+      f32x4 f[4];
+      if (is_whole(tile, valid)) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) f[b] = f32x4{1, 1, 1, 1} * __builtin_ldexpf(1.0f, -bump);
+      } else {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) f[b] = *reinterpret_cast<const f32x4*>(raw + Y::VG + 4 * (8 * b + 4 * hh));
+        if (masked) {
+#pragma unroll
+          for (int i2 = 0; i2 < 16; ++i2) f[i2 >> 2][i2 & 3] = sees(i2) ? f[i2 >> 2][i2 & 3] : 0.0f;
+        }
+        float smax = 0.0f;
+#pragma unroll
+        for (int i2 = 0; i2 < 16; ++i2) smax = fmaxf(smax, f[i2 >> 2][i2 & 3]);
+        const uint32_t bits = __float_as_uint(smax);
+        const auto sw = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+        const int e = max(bump, (int)(max(sw[0], sw[1]) >> 23) - 126 - e_ref);
+        if (__any(e > bump)) {
+          const float grow = __builtin_ldexpf(1.0f, bump - e);
+          bump = e;
+          bumped = true;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) acc[d] *= grow;
+        }
+#pragma unroll
+        for (int i2 = 0; i2 < 16; ++i2) f[i2 >> 2][i2 & 3] = __builtin_ldexpf(f[i2 >> 2][i2 & 3], -(e_ref + bump));
+      }
+#pragma unroll
+      for (int i2 = 0; i2 < 16; i2 += 2) {
+        const mxq_f32x2 pair = {(float)wf[i2 >> 3][i2 & 7] * f[i2 >> 2][i2 & 3],
+                                (float)wf[i2 >> 3][(i2 & 7) + 1] * f[i2 >> 2][(i2 & 3) + 1]};
+        const f16x2 hp = __builtin_convertvector(pair, f16x2);
+        wf[i2 >> 3][i2 & 7] = hp.x;
+        wf[i2 >> 3][(i2 & 7) + 1] = hp.y;
+      }
+    }
 #pragma unroll
     for (int v0 = 0; v0 < NV; v0 += 8) {
       if (v0) {
@@ -1065,11 +1150,29 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
       issue(p + 3, 3);
       // V' of this phase may be on a larger Sref than the sums
       if (e_fill > e_ref) {
-        const float grow = __builtin_ldexpf(1.0f, e_ref - e_fill);
+        const int up = e_fill - e_ref, take = min(bump, up);
+        const float grow = __builtin_ldexpf(1.0f, take - up);
         e_ref = e_fill;
+        bump -= take;
 #pragma unroll
         for (int d = 0; d < DT; ++d) acc[d] *= grow;
       }
+      // Whole tiles take sums on the shared Sref.  A bump up to 64 is undone: the sums
+      // stay below 2^15 2^16 2^30 2^64 (weight, V', tokens).  Columns with a larger one
+      // stay apart, and weigh by it.
+      if (__builtin_expect(bumped, 0)) {
+        const int tile = tiles.x + p * PH;
+        apart = (tile + PH > w0) & (tile < w1);
+        if (apart) {
+          const int back = bump <= 64 ? bump : 0;
+          const float grow = __builtin_ldexpf(1.0f, back);
+          bump -= back;
+          apart = bumped = __any(bump > 0);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) acc[d] *= grow;
+        }
+      }
+      whole_now = whole_next;
       scale_of(p + 1, 1);
 #pragma unroll 1
       for (int k = 0; k < 2 * PH; ++k) {
@@ -1086,7 +1189,7 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
     const auto sw = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
     l = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
   }
-  const float f = l == 0.0f ? 0.0f : __builtin_ldexpf(1.0f / l, e_ref - 4);
+  const float f = l == 0.0f ? 0.0f : __builtin_ldexpf(1.0f / l, e_ref + bump - 4);
   store_index(a, u, h);
   if (!have) return;
   const int64_t pr = ((int64_t)uid * cc.H + h) * Y::CT + wave * 32 + c;

@@ -139,3 +139,56 @@ def test_an_infinite_row_is_stored_as_nan(lens, news, grp, bad, which):
     rows = slice(p.offs[0], p.offs[1])
     assert out[rows].isnan().all() and not out[p.offs[1]:].isnan().any()
     assert lse[rows].isnan().all() if which == "k" else lse.isfinite().all()
+
+
+# several rows of a request, which see different tokens: drafted tokens and prompt chunks, whole and split, windows
+# that have passed a token for some rows only
+UNEVEN = [([40, 33], [3, 2], 4, 0, 128), ([40], [16], 1, 0, 64), ([3000], [7], 4, 0, 128), ([90], [9], 1, 20, 256),
+          ([70, 33], [30, 2], 2, 17, 128), ([300, 90], [100, 70], 4, 0, 128), ([3000], [150], 4, 0, 128),
+          ([700], [600], 1, 0, 64), ([700], [300], 4, 100, 128), ([2000], [400], 2, 333, 64), ([400], [150], 2, 90, 256),
+          ([3000], [300], 1, 900, 128), ([1500], [700], 1, 800, 256)]
+
+
+def _spoilt_tokens(p):
+    """Tokens that some rows of request 0 see and others do not: new ones, and ones that the window passes."""
+    n, new = p.lens[0], p.news[0]
+    for t in sorted({n - 1, n - (new + 1) // 2, n - new + 1} | ({n - new - p.window + 1 + new // 2} if p.window else set())):
+        sees = _sees(p, t)
+        yield t, sees
+        assert sees.any() and not sees[p.offs[0]:p.offs[1]].all()
+
+
+@pytest.mark.parametrize("lens,news,grp,window,d", UNEVEN)
+@pytest.mark.parametrize("kind", ["second scale", "block scale", "infinite"])
+def test_a_spoilt_value_is_kept_from_the_rows_that_do_not_see_it(kind, lens, news, grp, window, d):
+    """A NaN in a token's V row (by its second scale, or by the scale of a block) reaches the rows that see the token
+    and no others."""
+    p, cache = _shape(24, lens, news, grp, d=d, window=window)
+    want, want_lse = _call(p, cache)
+    p.check(want, want_lse)
+    for t, sees in _spoilt_tokens(p):
+        page, slot = _place(p, t)
+        at = cache.v_scales[page, 0, d // 16 - 1] if kind == "block scale" else cache.v_gscales[page, 0]
+        keep = at[slot].clone()
+        at[slot] = {"second scale": float("nan"), "infinite": float("inf"), "block scale": 0x7F}[kind]
+        out, lse = _call(p, cache)
+        at[slot] = keep
+        spoilt = ~out[sees].isfinite()
+        assert spoilt[..., -16:].all() if kind == "block scale" else spoilt.all(), t
+        _check_others(p, sees, out, want_lse, want, want_lse)
+        p.check(torch.where(sees[:, None, None], want, out), lse)      # log sums do not depend on V
+
+
+@pytest.mark.parametrize("lens,news,grp,window,d", UNEVEN)
+@pytest.mark.parametrize("power", [20, 60, 110])
+def test_a_large_value_costs_the_rows_that_do_not_see_it_nothing(power, lens, news, grp, window, d):
+    """One V row 2^power times the others: the bounds go by what a row sees."""
+    p, cache = _shape(25, lens, news, grp, d=d, window=window)
+    for t, sees in _spoilt_tokens(p):
+        page, slot = _place(p, t)
+        cache.v_gscales[page, 0, slot] *= 2.0 ** power
+        p.v[0][:, t] *= 2.0 ** power
+        out, lse = _call(p, cache)
+        cache.v_gscales[page, 0, slot] *= 2.0 ** -power
+        p.check(out, lse)
+        p.v[0][:, t] *= 2.0 ** -power
