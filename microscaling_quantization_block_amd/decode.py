@@ -51,10 +51,16 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-# The raw handle of a device's current stream and the current device: a decode
-# step is many short calls, and the objects around these cost as much as a call.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+def _device_calls():
+    """The raw handle of a device's current stream, and the current device.  A
+    decode step is many short calls, and the objects that the public functions
+    put around these two cost as much as a call; they serve where torch has not
+    the short ones (a build without a GPU, another version)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return raw, getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+_raw_stream, _current_device = _device_calls()
 
 
 def _launch(device, fn, *args):

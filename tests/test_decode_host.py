@@ -3,6 +3,7 @@
 import os
 import shutil
 import subprocess
+import sys
 
 import pytest
 
@@ -26,3 +27,30 @@ def test_rows_and_requests_agree(tmp_path):
     assert r.returncode == 0, r.stderr[-3000:]
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout[-2000:] + r.stderr[-2000:]
+
+
+def test_import_without_gpu_support_in_torch():
+    """The package imports under a torch built without a GPU, whose private bindings are not there."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import microscaling_quantization_block_amd as m\n"
+            "assert m.nvfp4_attention and m.NVFP4Cache\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_launches_without_the_private_bindings(monkeypatch):
+    """Where torch lacks the short bindings, the public calls give the device and the stream."""
+    import torch
+    from microscaling_quantization_block_amd import decode
+
+    class Stream:
+        cuda_stream = 0x1234
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream if device == 0 else None)
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    raw_stream, current_device = decode._device_calls()
+    assert current_device() == 0 and raw_stream(0) == 0x1234
