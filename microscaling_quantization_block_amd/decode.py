@@ -161,8 +161,10 @@ def _gemv(fn, x, w, M, N, K, weight_rows, out, group_row_offsets, x_row_index):
         _check_tensor(out, "out", torch.bfloat16, 2, dev)
         if out.shape[0] < M or out.shape[1] < N or out.stride(1) != 1:
             raise ValueError(f"out must hold [{M}, {N}] with unit column stride")
-    _launch(dev, fn, x.data_ptr(), x.stride(0), x.shape[0], ctypes.byref(w._c()), M, N, K, out.data_ptr(),
-            out.stride(0), ng, _p(group_row_offsets), _p(x_row_index))
+    # the stride of a single row means nothing
+    ld_x, ld_y = x.stride(0) if x.shape[0] > 1 else K, out.stride(0) if out.shape[0] > 1 else N
+    _launch(dev, fn, x.data_ptr(), ld_x, x.shape[0], ctypes.byref(w._c()), M, N, K, out.data_ptr(), ld_y, ng,
+            _p(group_row_offsets), _p(x_row_index))
     return out
 
 
@@ -251,7 +253,8 @@ def _check_requests(cache, block_table, seq_lens, q_offsets, rows):
 
 
 def _check_rows(t, name, heads, d, rows, dev):
-    """[rows, heads, d] BF16 with unit stride along d (heads None: any); returns heads and the two strides."""
+    """[rows, heads, d] BF16 with unit stride along d (heads None: any); returns heads and the two strides (0 for a
+    single row or head, whose stride means nothing)."""
     if not _is(t, torch.bfloat16, 3, dev):
         _check_tensor(t, name, torch.bfloat16, 3, dev)
     shape, (st, sh, sd) = t.shape, t.stride()
@@ -259,7 +262,7 @@ def _check_rows(t, name, heads, d, rows, dev):
         raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {tuple(shape)}")
     if sd != 1:
         raise ValueError(f"{name} must have unit stride along head_dim")
-    return shape[1], st, sh
+    return shape[1], st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
 
 
 @_takes_stream

@@ -192,3 +192,27 @@ def test_a_large_value_costs_the_rows_that_do_not_see_it_nothing(power, lens, ne
         cache.v_gscales[page, 0, slot] *= 2.0 ** -power
         p.check(out, lse)
         p.v[0][:, t] *= 2.0 ** -power
+
+
+def test_one_row_of_any_stride():
+    """A size of one has a stride that means nothing: one row of x, of y, of q, one head."""
+    m, rng = _m(), np.random.default_rng(26)
+    n, k = 48, 64
+    w = R.Weight(rng, n, k)
+    x = to_dev_bf16(R.bf16(rng, (1, k)))
+    odd = torch.empty_strided((1, k), (3, 1), dtype=torch.bfloat16, device="cuda").copy_(x)
+    out = torch.empty_strided((1, n), (1, 1), dtype=torch.bfloat16, device="cuda")
+    say("one row")
+    want = m.nvfp4_gemv(x, w.operand(m, torch), 1, n, k)
+    m.nvfp4_gemv(odd, w.operand(m, torch), 1, n, k, out=out)
+    assert torch.equal(out, want)
+    p = Problem(27, 64, 1, 1, 16, [40], [1])
+    cache = p.cache.device(m, torch)
+    q = to_dev_bf16(p.q)
+    odd = torch.empty_strided((1, 1, 64), (3, 5, 1), dtype=torch.bfloat16, device="cuda").copy_(q)
+    out = torch.empty_strided((1, 1, 64), (7, 9, 1), dtype=torch.bfloat16, device="cuda")
+    args = cache, _dev(p.table), _dev(p.lens)
+    want = m.nvfp4_attention(q, *args)
+    m.nvfp4_attention(odd, *args, out=out)
+    assert torch.equal(out, want)
+    m.nvfp4_cache_append(odd, odd, *args)
