@@ -32,6 +32,8 @@ extern "C" {
  *   x_row_index    device int32 [M] or NULL: row m reads x row x_row_index[m];
  *                  an entry outside [0, x_rows) reads a row of zeros
  *   x_rows         rows of x (== M when x_row_index is NULL)
+ * Sums run over x value(c) s_b, S multiplies them at the end: x below 2^100 in
+ * magnitude (for K up to 2^16).
  * Shapes: K % 16 == 0; N % 16 == 0 (TILE), N % 32 == 0 and K % 64 == 0 (MFMA).
  * Alignment: x and the codes 16-byte aligned, ld_x % 8 == 0, w->ld % 16 == 0.
  */
@@ -115,7 +117,11 @@ mxq_status nvfp4_cache_append(const uint16_t* k, int64_t k_token_stride, int64_t
  * out = sum_t softmax(x)_t dq(V_t).  A row with nothing in reach (an empty
  * request, more rows than tokens, no pages) gives zeros and lse -infinity.
  * The rows' own K and V are read from the cache: append first.  Cache bytes
- * no row reaches may hold anything.
+ * no row reaches may hold anything, and what one row reaches does not touch the
+ * rows that do not.  A NaN or an infinity in a row of q, or a NaN in a K or V row that
+ * it reaches (a NaN among a token's V scales may spoil all of that row's values), makes
+ * the row NaN, by q or K the log sum too.  Second scales are finite or NaN and not
+ * negative, as nvfp4_cache_append stores them; K below 2^100 in magnitude.
  *   q, out       BF16 [tokens, num_q_heads, head_dim], strides in elements
  *                (multiples of 8), head_dim contiguous, 16-byte aligned
  *   lse          NULL, or binary32 [tokens, num_q_heads] contiguous: the natural

@@ -9,11 +9,18 @@
 // exactly; a query row is scaled by a power of two to have its largest element
 // in [2^13, 2^14), which keeps its eight significant bits down to 2^-27 of that
 // element.  S of K multiplies the logit, in binary32.  S of V is brought near
-// one by Sref, a running power of two above every S_t seen, and goes to the
-// weights w_t = p_t S_t / Sref (few columns: fewer weights than values) or to the
-// values (many columns: the dequantized tile is shared); either is one rounding
-// to FP16, 2^-11 relative.  Sums, maxima and logits are binary32, and l sums
-// the exponentials before they are rounded.
+// one by Sref, a running power of two above every S_t seen.  With few columns it
+// goes to the weights (fewer than the values), w_t = fp16(p_t S_t / Sref): one
+// rounding, 2^-11 relative.  With many the dequantized tile is shared, and it goes
+// to the values: fp16(p_t) meets fp16(c fp16(s_b S_t 2^4 / Sref)), three roundings,
+// which keep the matrix instruction at FP16 and the weights free of a factor per
+// token.  Below 2^-14 of the scale that a weight or value has, 2^-25 absolute takes
+// the place of 2^-11.  Sums, maxima and logits are binary32, and l sums the
+// exponentials before they are rounded.
+//
+// The ranges: q . k of the scaled row passes binary32 before the row's factor is
+// applied, so keys must stay below 2^100 in magnitude; V rows below 2^-90 are not
+// scaled up any further, and lose bits to FP16 (2^-124 of absolute error a token).
 //
 // What a column does not reach must not count, whatever it holds.  Its logit is
 // replaced by -infinity; but V's values are shared by the columns of a tile, and

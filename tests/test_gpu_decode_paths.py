@@ -87,3 +87,23 @@ def test_streamed_rows_between_one_and_two_thousand(op, block, layout, m_rows, k
 @pytest.mark.parametrize("op", ["gemv", "swiglu"])
 def test_two_rows_of_longer_weights(op, block, layout, k):
     _dense(op, 2, 96, k, block, layout, k)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,news,grp", [([257, 100, 33], [1, 1, 1], 4), ([300, 64], [3, 2], 2), ([2900], [1], 8)])
+def test_few_columns_round_once(d, lens, news, grp):
+    """The kernel for few columns rounds the weights to FP16 and nothing else: the values c s_b are FP16 numbers, and
+    the second scale goes to the weight before it is rounded.  So one rounding of 2^-11 where decode_ref has three."""
+    from oracle import formats as F
+    from tests.util import from_dev_bf16
+    p = Problem(36, d, 1, grp, 32, lens, news)
+    out, lse = p.run()
+    p.check(out, lse)
+    got, qv = F.bf16_bits_to_f64(from_dev_bf16(out)), F.bf16_bits_to_f64(p.q)
+    for b, (n, new) in enumerate(zip(lens, news)):
+        rows, pos = slice(p.offs[b], p.offs[b + 1]), n - new + np.arange(new)
+        for h in range(grp):
+            o, _, tol, _ = R.attention_ref(qv[rows, h], p.k[b][0], p.v[b][0], pos, p.scale, 0)
+            mass = R.attention_ref(qv[rows, h], p.k[b][0], np.abs(p.v[b][0]), pos, p.scale, 0)[0]
+            tight = tol - (1 + R.EPS_BF16) * 2 * R.EPS_FP16 * mass
+            assert (tight > 0).all() and (np.abs(got[rows, h] - o) <= tight).all(), (b, h)
