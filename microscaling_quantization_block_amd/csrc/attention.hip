@@ -1224,13 +1224,14 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int CT)
   const int64_t row = ((int64_t)blockIdx.x * 4 + wave) / RW, rows = a.T * a.Hq;
   if (row >= rows) return;
   const int64_t tq = row / a.Hq, head = row - tq * a.Hq;
-  const int64_t b = request_of(a.c, tq, a.T);
+  RequestRows own;
+  const int64_t b = request_of(a.c, tq, a.T, own);
   if (b < 0) return;                           // a row of no request is left as it was
   const int2 ix = a.part_index[b];
   const int chunks = ix.y;
   if (chunks <= 1) return;                     // written by its only chunk
   const int h = (int)(head / a.G);
-  const int64_t j = (tq - (a.c.q_offsets ? a.c.q_offsets[b] : tq)) * a.G + (head - (int64_t)h * a.G);
+  const int64_t j = (tq - own.begin) * a.G + (head - (int64_t)h * a.G);
   const int64_t stride = (int64_t)a.c.H * CT;  // of a chunk
   const int64_t unit = ix.x + j / CT * chunks;  // of chunk 0
   if (unit < 0 || unit + chunks > a.units) return;   // offsets out of order name more units than the grid has

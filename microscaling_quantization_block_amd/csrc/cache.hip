@@ -41,10 +41,10 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
   const int64_t h = is_v ? hv - c.H : hv;
   const uint16_t* src = is_v ? a.v + t * a.v_token + h * a.v_head : a.k + t * a.k_token + h * a.k_head;
   const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * lane);
-  const int64_t b = request_of(c, t, a.T);
+  RequestRows rows;
+  const int64_t b = request_of(c, t, a.T, rows);
   if (b < 0) return;
-  const int64_t q_end = c.q_offsets ? c.q_offsets[b + 1] : t + 1;
-  const int64_t pos = c.seq_lens[b] - q_end + t;
+  const int64_t pos = (int64_t)c.seq_lens[b] - rows.len + (t - rows.begin);
   const int64_t page = page_of(c, b, pos);
 
   const uint32_t m8 = amax8_bits(x);

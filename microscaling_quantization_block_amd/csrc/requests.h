@@ -21,10 +21,11 @@ __host__ __device__ inline RequestRows request_rows(const CacheArgs& c, int64_t 
   return r;
 }
 
-// The request that owns row t: the largest b with q_offsets[b] <= t, -1 if t lies
-// in no request (rows before the first or behind the last, and those whose
-// request has no rows by the rule above).
-__host__ __device__ inline int64_t request_of(const CacheArgs& c, int64_t t, int64_t T) {
+// The request that owns row t and its rows: the largest b with q_offsets[b] <= t,
+// -1 if t lies in no request (rows before the first or behind the last, and those
+// whose request has no rows by the rule above).
+__host__ __device__ inline int64_t request_of(const CacheArgs& c, int64_t t, int64_t T, RequestRows& rows) {
+  rows = {(int)t, 1};
   if (!c.q_offsets) return t < c.B ? t : -1;
   if (t < c.q_offsets[0] || t >= c.q_offsets[c.B]) return -1;
   int64_t lo = 0, hi = c.B;                    // q_offsets[lo] <= t < q_offsets[hi]
@@ -33,7 +34,8 @@ __host__ __device__ inline int64_t request_of(const CacheArgs& c, int64_t t, int
     if (c.q_offsets[mid] <= t) lo = mid;
     else hi = mid;
   }
-  return request_rows(c, lo, T).len ? lo : -1;
+  rows = request_rows(c, lo, T);
+  return rows.len ? lo : -1;
 }
 
 }  // namespace mxq

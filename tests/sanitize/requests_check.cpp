@@ -31,10 +31,11 @@ int main() {
       }
     }
     for (int t = 0; t < T; ++t, ++cases) {
-      const int64_t b = mxq::request_of(c, t, T);
+      mxq::RequestRows own;
+      const int64_t b = mxq::request_of(c, t, T, own);
       if (b >= 0) {
         const mxq::RequestRows r = mxq::request_rows(c, b, T);
-        if (b >= B || t < r.begin || t >= r.begin + r.len) {
+        if (b >= B || own.begin != r.begin || own.len != r.len || t < r.begin || t >= r.begin + r.len) {
           printf("run %d row %d: owner %d has rows %d + %d\n", run, t, (int)b, r.begin, r.len);
           return 1;
         }
