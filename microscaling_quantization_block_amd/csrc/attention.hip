@@ -42,11 +42,16 @@
 //
 // Two kernels, by the query columns (row, head of the KV head's group) of a
 // request, and a join where contexts are split.  With few columns the cache's
-// bytes bound it: 64 requests of up to 4096 tokens, 177 MB, 55.6 us (3.2 TB/s);
-// four of up to 131071, 393 MB, 91.7 us (4.3 TB/s, a large copy has 4.8).  With
+// bytes bound it, and the vector instructions that unpack them: 64 requests of up
+// to 4096 tokens, 177 MB, 56.0 us (3.2 TB/s); four of up to 131071, 393 MB, 91 us
+// (4.3 TB/s, a large copy has 4.8).  With
 // many the matrix and vector units do: prompt chunks of 2048 rows behind 8192
-// tokens, 437 GF, 784 us (558 TF/s).  A single short request is latency: 11.7
-// us, the join's launch included.
+// tokens, 437 GF, 791 us (553 TF/s).  A single short request is latency: 11.8
+// us, the join's launch included.  Border tiles cost most where there is little
+// else: four prompts of up to 512 tokens, 16 heads, 41.8 us (37.2 without what keeps
+// their columns apart).  With head_dim 256 the kernel for many columns has more to
+// hold than the registers do (q's fragments come back from scratch in the loop):
+// chunks of 2048 rows behind 8192 tokens, 16 heads, 437 GF, 2057 us.
 
 #include "cache_device.h"
 #include "mxq_kernels.h"

@@ -12,7 +12,7 @@
 // maximum over the lanes.  A decode step (128 rows of 8 heads, 3.6 us) is one
 // chain of latencies: request, offsets, page, store.  A prompt (10 k tokens of 8 heads)
 // is bound by memory:
-// 91 MB of rows, codes and dequantized rows in 29.7 us, 3.1 TB/s, where a large
+// 91 MB of rows, codes and dequantized rows in 30.1 us, 3.0 TB/s, where a large
 // copy has 4.8; its rows are written as short pieces of many pages.
 //
 // V's block scales are stored [D / 16, P] inside a page (K's [P, D / 16]):
