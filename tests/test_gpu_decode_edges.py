@@ -216,3 +216,26 @@ def test_one_row_of_any_stride():
     m.nvfp4_attention(odd, *args, out=out)
     assert torch.equal(out, want)
     m.nvfp4_cache_append(odd, odd, *args)
+
+
+@pytest.mark.parametrize("d,news,window", [(64, [90, 2], 0), (128, [90, 40], 0), (128, [200], 60), (256, [70, 1], 0),
+                                           (128, [2, 3], 0)])
+def test_holes_among_seen_tokens(d, news, window):
+    """Pages missing in the middle of contexts that many columns see, with a NaN and a large V row around them."""
+    lens = [250, 77][:len(news)]
+    table = np.full((len(news), 16), -1, np.int32)
+    table[0] = [0, 1, -1, 3, 4, 99, 5, 6, -7, 7, 8, -1, 9, 10, 11, 12]
+    if len(news) > 1:
+        table[1, :5] = [13, -1, 14, 15, 16]
+    p = Problem(28, d, 1, 2, 16, lens, news, window=window, table=table, pages=17)
+    cache = p.cache.device(_m(), torch)
+    want, want_lse = _call(p, cache)
+    p.check(want, want_lse)
+    t = lens[0] - 1
+    page, slot = _place(p, t)
+    sees = _sees(p, t)
+    for bad in (float("nan"), 2.0 ** 80):
+        cache.v_gscales[page, 0, slot] = bad
+        out, lse = _call(p, cache)
+        assert out[sees].isnan().any() == (bad != bad)
+        _check_others(p, sees, out, lse, want, want_lse)
