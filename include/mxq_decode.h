@@ -120,7 +120,7 @@ mxq_status nvfp4_cache_append(const uint16_t* k, int64_t k_token_stride, int64_t
  * no row reaches may hold anything, and what one row reaches does not touch the
  * rows that do not.  A NaN or an infinity in a row of q, or a NaN in a K or V row that
  * it reaches (a NaN among a token's V scales may spoil all of that row's values), makes
- * the row NaN, by q or K the log sum too.  Second scales are finite or NaN and not
+ * the row NaN, by q or K the log sum too; so does a largest x_t beyond binary32.  Second scales are finite or NaN and not
  * negative, as nvfp4_cache_append stores them; K below 2^100 in magnitude.
  *   q, out       BF16 [tokens, num_q_heads, head_dim], strides in elements
  *                (multiples of 8), head_dim contiguous, 16-byte aligned

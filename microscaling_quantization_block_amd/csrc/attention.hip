@@ -137,6 +137,14 @@ __device__ __forceinline__ float max_groups(float v) {
   return max2(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
+// BASE less a maximum top (in units of cs): 0 for a column that has nothing in
+// reach yet (every exponential is 0), NaN for a logit beyond binary32: against an
+// infinite maximum every exponential would be 0, as if nothing were in reach.
+__device__ __forceinline__ float base_less(float top, float cs) {
+  const float r = top * cs;
+  return top == NEG_INF ? BASE : fabsf(r) < __builtin_inff() ? BASE - r : __builtin_nanf("");
+}
+
 // Eight codes of K times their block scale sv.
 __device__ __forceinline__ f16x8 k_fragment(uint32_t w, _Float16 scale) {
   const f16x2 sv = {scale, scale};
@@ -391,7 +399,7 @@ __device__ __forceinline__ bool move_maxima(Columns<D, NQ>& o, const f32x4 (*x)[
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const float top = max2(o.m[n], max_groups(mx[n]));
-    const float mu = top == NEG_INF ? BASE : BASE - top * o.cs[n];   // nothing in reach yet: every exponential is 0
+    const float mu = base_less(top, o.cs[n]);
     alpha[n] = __builtin_amdgcn_exp2f(__builtin_fmaf(o.m[n], o.cs[n], mu - BASE));
     o.m[n] = top;
     o.mu[n] = mu;
@@ -1079,7 +1087,7 @@ __global__ __launch_bounds__(64 * MANY_WAVES, 2) void attention_many_kernel(Attn
       const uint32_t bits = __float_as_uint(mx);
       const auto sw = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
       const float top = max2(m, max2(__uint_as_float(sw[0]), __uint_as_float(sw[1])));
-      const float mu_new = top == NEG_INF ? BASE : BASE - top * cs;
+      const float mu_new = base_less(top, cs);
       const float alpha = __builtin_amdgcn_exp2f(__builtin_fmaf(m, cs, mu_new - BASE));
       m = top;
       mu = mu_new;

@@ -239,3 +239,16 @@ def test_holes_among_seen_tokens(d, news, window):
         out, lse = _call(p, cache)
         assert out[sees].isnan().any() == (bad != bad)
         _check_others(p, sees, out, lse, want, want_lse)
+
+
+@pytest.mark.parametrize("lens,news,grp", SHAPES)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_logits_beyond_binary32_are_nan(lens, news, grp, sign):
+    """q . k of 2^140: no finite logit, so no finite answer (and not that of an empty context)."""
+    p, _ = _shape(29, lens, news, grp, k_scale=2.0 ** 70)
+    p.scale = sign
+    p.cache.t["k_codes"][...] &= 0x77                         # all keys positive
+    q = to_dev_bf16(p.q)
+    q[0, 0] = 2.0 ** 70
+    out, lse = _call(p, p.cache.device(_m(), torch), q)
+    assert out[0, 0].isnan().all() and lse[0, 0].isnan()
