@@ -55,8 +55,8 @@ mxq_status nvfp4_gemv_swiglu(const uint16_t* x, int64_t ld_x, int64_t x_rows, co
 
 /*
  * A paged NVFP4 cache of K and V rows (a row: the head_dim values of one token
- * and KV head, quantized as nvfp4_quantize does a row, nearest even, one second
- * scale per row).  Inside a page everything is contiguous:
+ * and KV head, quantized as nvfp4_quantize does a row of finite values, nearest
+ * even, one second scale per row).  Inside a page everything is contiguous:
  *   k_codes, v_codes      [num_heads, page_size, head_dim / 2] bytes, low nibble even
  *   k_scales              [num_heads, page_size, head_dim / 16] E4M3
  *   v_scales              [num_heads, head_dim / 16, page_size] E4M3 (the
@@ -87,8 +87,8 @@ typedef struct {
  *   seq_lens    [num_requests]: tokens of each request, the new ones included
  *   q_offsets   [num_requests + 1] or NULL: request b has the call's rows
  *               [q_offsets[b], q_offsets[b+1]), non-decreasing, within
- *               [0, tokens]; row i of them is
- *               position seq_lens[b] - (their number) + i.  NULL: one row per
+ *               [0, tokens]; row i of them is position
+ *               seq_lens[b] - (their number) + i.  NULL: one row per
  *               request (tokens == num_requests).  Rows before q_offsets[0] or
  *               from the last offset on belong to no request, and a request
  *               whose offsets leave [0, tokens] has no rows: nothing is read
@@ -118,17 +118,18 @@ mxq_status nvfp4_cache_append(const uint16_t* k, int64_t k_token_stride, int64_t
  * request, more rows than tokens, no pages) gives zeros and lse -infinity.
  * The rows' own K and V are read from the cache: append first.  Cache bytes
  * no row reaches may hold anything, and what one row reaches does not touch the
- * rows that do not.  A NaN or an infinity in a row of q, or a NaN in a K or V row that
- * it reaches (a NaN among a token's V scales may spoil all of that row's values), makes
- * the row NaN, by q or K the log sum too; so does a largest x_t beyond binary32.  Second scales are finite or NaN and not
- * negative, as nvfp4_cache_append stores them; K below 2^100 in magnitude.
+ * rows that do not.  A row becomes NaN by a NaN or an infinity in its q, by a NaN
+ * in a K or V row that it reaches (a NaN among a token's V scales may spoil all of
+ * that token's values), and by a largest x_t beyond binary32; its log sum too,
+ * but for V.  Second scales are finite or NaN and not negative, as
+ * nvfp4_cache_append stores them; K below 2^100 in magnitude.
  *   q, out       BF16 [tokens, num_q_heads, head_dim], strides in elements
  *                (multiples of 8), head_dim contiguous, 16-byte aligned
  *   lse          NULL, or binary32 [tokens, num_q_heads] contiguous: the natural
  *                log of sum_t exp(x_t)
  *   workspace    device, 16-byte aligned, nvfp4_attention_workspace() bytes (may
- *                be NULL if that is 0; a window may need less); its content before and after means
- *                nothing, calls in flight at once need one each
+ *                be NULL if that is 0; a window may need less); its content
+ *                before and after means nothing, calls in flight at once need one each
  * How the context is split follows from the shapes alone (table_width bounds
  * the lengths), so a captured call replays for any lengths, and equal calls
  * give equal bits.
