@@ -1,26 +1,13 @@
 // New K and V rows into the pages of an NVFP4 cache.
 //
-// A row is the D values of one token and KV head.  It is quantized exactly as
-// nvfp4_quantize does a row under a per-row second scale (nearest even):
-// S = fl(amax / 2688), s_b = E4M3(fl(a_b / fl(6 S))), codes E2M1 of
-// fl(x fl(1 / fl(s_b S))).  One with an infinity or a NaN gets a NaN for S:
-// every value of it is NaN then, and the attention meets no infinite second scale,
-// whose logits might be -infinity and look like tokens out of reach.
-//
-// D / 8 lanes hold a row, eight values each (one
-// 16-byte load), a block is a lane pair; the row maximum is an integer
-// maximum over the lanes.  A decode step (128 rows of 8 heads, 3.6 us) is one
+// D / 8 lanes hold a row, eight values each (one 16-byte load); what they store
+// is append_row's (cache_device.h).  A decode step (128 rows of 8 heads, 3.6 us) is one
 // chain of latencies: request, offsets, page, store.  A prompt (10 k tokens of 8 heads)
 // is bound by memory:
 // 91 MB of rows, codes and dequantized rows in 30.1 us, 3.0 TB/s, where a large
 // copy has 4.8; its rows are written as short pieces of many pages.
-//
-// V's block scales are stored [D / 16, P] inside a page (K's [P, D / 16]):
-// the attention kernel contracts over tokens there and reads the scales of
-// four neighbouring tokens of one block as one word.
 
 #include "cache_device.h"
-#include "nvfp4_device.h"
 
 namespace mxq {
 
@@ -47,43 +34,8 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
   const int64_t pos = (int64_t)c.seq_lens[b] - rows.len + (t - rows.begin);
   const int64_t page = page_of(c, b, pos);
 
-  const uint32_t m8 = amax8_bits(x);
-  const uint32_t a_b = umax(m8, lane_xor_u32(m8, 1));
-  uint32_t amax = a_b;
-#pragma unroll
-  for (int s = 2; s < L; s *= 2) amax = umax(amax, lane_xor_u32(amax, s));
-  // a row with an infinity or a NaN: all its values are NaN
-  const float S = amax < 0x7F800000u ? __uint_as_float(amax) / 2688.0f : __builtin_nanf("");
-  const BlockScale bs = nv_block_scale(__uint_as_float(a_b), S);
-  const u32x4 none = {0, 0, 0, 0};
-  const uint32_t code = S < TINY_S ? nv_encode8<false, true>(x, bs.r, none) : nv_encode8<false, false>(x, bs.r, none);
-
-  if (page >= 0) {
-    const int P = 1 << c.P_log2;
-    const int64_t slot = pos & (P - 1);
-    const int64_t hs = h * P + slot;           // the row's index in the page
-    uint8_t* codes = (is_v ? c.vc : c.kc) + page * c.pc + hs * (D / 2);
-    *reinterpret_cast<uint32_t*>(codes + 4 * lane) = code;
-    if ((lane & 1) == 0) {
-      if (is_v) c.vs[page * c.psc + (h * (D / 16) + (lane >> 1)) * P + slot] = (uint8_t)bs.code;
-      else c.ks[page * c.psc + hs * (D / 16) + (lane >> 1)] = (uint8_t)bs.code;
-    }
-    if (lane == 0) (is_v ? c.vg : c.kg)[page * c.pg + hs] = S;
-  }
   uint16_t* dq = is_v ? a.v_dq : a.k_dq;
-  if (dq) {
-    // bf16(fl(fl(c s_b) S)), the dequantizer's chain
-    const float sb = e4m3_to_f32(bs.code);
-    mxq_f32x2 v[4];
-    v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 0);
-    v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 1);
-    v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 2);
-    v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 3);
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = f32x2_to_bf16x2((v[i].x * sb) * S, (v[i].y * sb) * S);
-    *reinterpret_cast<uint4*>(dq + (t * c.H + h) * D + 8 * lane) = make_uint4(o[0], o[1], o[2], o[3]);
-  }
+  append_row<D>(c, is_v, h, page, pos, lane, x, dq ? dq + (t * c.H + h) * D : nullptr);
 }
 
 hipError_t launch_cache_append(const AppendArgs& a, hipStream_t st) {

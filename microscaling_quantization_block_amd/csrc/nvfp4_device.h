@@ -78,6 +78,20 @@ __device__ __forceinline__ uint32_t nv_encode8(uint4 v, float r, u32x4 draws) {
   return out;
 }
 
+// BF16 of the values that 8 nibbles stand for, bf16(fl(fl(c s_b) S)): the
+// dequantizer's chain (c s_b is exact).
+__device__ __forceinline__ uint4 nv_decode8(uint32_t code, float sb, float S) {
+  mxq_f32x2 v[4];
+  v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 0);
+  v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 1);
+  v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 2);
+  v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 3);
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = f32x2_to_bf16x2((v[i].x * sb) * S, (v[i].y * sb) * S);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // Calls f(std::true_type) when S is below 2^-64 (the scaled frame), else
 // f(std::false_type).  S is wave-uniform at every call site.
 template <class F>
