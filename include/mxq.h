@@ -562,5 +562,6 @@ int mxq_version(void);
 #endif
 
 #include "mxq_decode.h"   /* few-row products, the NVFP4 cache and attention over it */
+#include "mxq_layer.h"    /* the norm, the router and the experts' rows, the rotated cache append */
 
 #endif /* MXQ_H */

@@ -1,0 +1,11 @@
+// Host-only stand-ins for the launchers of the steps around a layer's products
+// (see host_stubs.cpp).
+#include "layer_kernels.h"
+
+namespace mxq {
+
+hipError_t launch_rmsnorm(const NormArgs&, mxq_format, hipStream_t) { return hipErrorNoDevice; }
+int64_t norm_bwd_groups(int64_t rows, int64_t) { return rows < 256 ? rows : 256; }
+hipError_t launch_rmsnorm_backward(const NormBwdArgs&, hipStream_t) { return hipErrorNoDevice; }
+
+}  // namespace mxq

@@ -1,0 +1,151 @@
+"""The steps around a layer's products without a GPU: include/mxq_layer.h and the library agree, invalid arguments are
+refused on the host with the documented status, and the binding checks what the device reads unvalidated.  Nothing is
+launched."""
+
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+import sys
+import tempfile
+
+import pytest
+import torch
+
+from tests.util import ROOT
+
+FAKE = ctypes.c_void_p(0x10000)       # never dereferenced: validation fails first
+ODD = ctypes.c_void_p(0x10008)
+EINVAL, ESHAPE, EALIGN, EUNSUPPORTED = 1, 2, 3, 4
+NAMES = ["mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace"]
+
+
+def _lib():
+    import microscaling_quantization_block_amd as m
+    from microscaling_quantization_block_amd import layer
+    sanitized = os.environ.get("MXQ_TEST_SANITIZED_LIBRARY")
+    if sanitized:
+        m.library_path = sanitized
+    if not os.path.exists(m.library_path):
+        pytest.skip("libmxq.so not built (run __graft_entry__.build())")
+    return m, layer._lib()
+
+
+def test_header_and_library_agree():
+    m, L = _lib()
+    text = open(os.path.join(ROOT, "include", "mxq_layer.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    declared = re.findall(r"^(?:mxq_status|int64_t)\s+(\w+)\s*\(", text, flags=re.M)
+    assert sorted(declared) == sorted(NAMES)
+    for n in declared:
+        assert hasattr(L, n) and hasattr(m, n) and n in m.__all__
+
+
+def test_norm_rejects_bad_arguments():
+    m, L = _lib()
+    Fm, Lay = m.Format, m.Layout
+
+    def call(x=FAKE, ld_x=256, r=None, ld_r=256, w=FAKE, rows=32, cols=256, eps=1e-6, h=None, ld_h=256, y=FAKE, ld_y=256,
+             rstd=None, fmt=Fm.BF16, layout=Lay.LINEAR, codes=None, ld_c=256, scales=None, gs=None, dq=None, ld_dq=256):
+        return L.mx_rmsnorm(x, ld_x, r, ld_r, w, rows, cols, eps, h, ld_h, y, ld_y, rstd, fmt, layout, codes, ld_c, scales,
+                            gs, dq, ld_dq, None)
+
+    fp8 = dict(fmt=Fm.MXFP8, codes=FAKE, scales=FAKE)
+    nv = dict(fmt=Fm.NVFP4, codes=FAKE, scales=FAKE, gs=FAKE)
+    f32s = dict(fmt=Fm.FP8_B128_F32, codes=FAKE, scales=FAKE)
+    for kw in (dict(x=None), dict(w=None), dict(y=None), dict(rows=-1), dict(cols=-8), dict(eps=-1.0),
+               dict(eps=float("nan")), dict(eps=float("inf")), dict(ld_x=248), dict(ld_y=248), dict(h=FAKE),
+               dict(r=FAKE, ld_r=248), dict(r=FAKE, h=FAKE, ld_h=248), dict(fmt=9), dict(fmt=-1), dict(layout=2),
+               dict(codes=FAKE), dict(scales=FAKE), dict(gs=FAKE), dict(dq=FAKE), dict(fp8, codes=None),
+               dict(fp8, scales=None), dict(fp8, gs=FAKE), dict(nv, gs=None), dict(fp8, ld_c=240), dict(nv, ld_c=112),
+               dict(fp8, dq=FAKE, ld_dq=248)):
+        assert call(**kw) == EINVAL, kw
+        assert "mx_rmsnorm" in m.lib().mxq_last_error().decode()
+    for kw in (dict(cols=252), dict(fp8, cols=240), dict(nv, cols=248), dict(f32s, cols=192), dict(fp8, layout=1, rows=31),
+               dict(fp8, layout=1, cols=96), dict(nv, layout=1, cols=96)):
+        assert call(**kw) == ESHAPE, kw
+    for kw in (dict(x=ODD), dict(w=ODD), dict(y=ODD), dict(ld_x=260), dict(ld_y=260), dict(r=ODD), dict(r=FAKE, ld_r=260),
+               dict(r=FAKE, h=ODD), dict(rstd=ctypes.c_void_p(0x10002)), dict(fp8, codes=ODD), dict(fp8, ld_c=264),
+               dict(nv, gs=ctypes.c_void_p(0x10002)), dict(f32s, scales=ctypes.c_void_p(0x10002)), dict(fp8, dq=ODD),
+               dict(fp8, dq=FAKE, ld_dq=260)):
+        assert call(**kw) == EALIGN, kw
+    for kw in (dict(cols=32776, ld_x=32776, ld_y=32776), dict(rows=1 << 31), dict(f32s, layout=1),
+               dict(fmt=Fm.FP8_B128, codes=FAKE, scales=FAKE, layout=1), dict(layout=1)):
+        assert call(**kw) == EUNSUPPORTED, kw
+    assert call(rows=0, x=None, y=None) == 0 and call(cols=0, x=None) == 0      # nothing to do, nothing launched
+
+
+def test_norm_backward_rejects_bad_arguments():
+    m, L = _lib()
+    big = 1 << 40
+
+    def call(dy=FAKE, ld_dy=64, h=FAKE, ld_h=64, w=FAKE, rstd=FAKE, dr=None, ld_dr=64, rows=5, cols=64, dx=FAKE, ld_dx=64,
+             dw=FAKE, ws=FAKE, ws_bytes=big):
+        return L.mx_rmsnorm_backward(dy, ld_dy, h, ld_h, w, rstd, dr, ld_dr, rows, cols, dx, ld_dx, dw, ws, ws_bytes, None)
+
+    for kw in (dict(dy=None), dict(h=None), dict(w=None), dict(rstd=None), dict(dx=None), dict(rows=-1), dict(cols=-8),
+               dict(ld_dy=56), dict(ld_h=56), dict(ld_dx=56), dict(dr=FAKE, ld_dr=56), dict(ws=None), dict(ws_bytes=1279)):
+        assert call(**kw) == EINVAL, kw
+    assert "workspace" in m.lib().mxq_last_error().decode()
+    for kw in (dict(dy=ODD), dict(h=ODD), dict(w=ODD), dict(dx=ODD), dict(dr=ODD), dict(ld_dy=68), dict(dw=ODD), dict(ws=ODD),
+               dict(rstd=ctypes.c_void_p(0x10002))):
+        assert call(**kw) == EALIGN, kw
+    assert call(cols=60) == ESHAPE and call(cols=32776, ld_dy=32776, ld_h=32776, ld_dx=32776) == EUNSUPPORTED
+    assert call(rows=1 << 31) == EUNSUPPORTED
+    assert call(rows=0, dw=None, ws=None) == 0 and call(cols=0) == 0
+    ws = m.mx_rmsnorm_backward_workspace
+    assert ws(5, 64) == 5 * 64 * 4 and ws(0, 64) == 0 and ws(-1, 64) == 0 and ws(1 << 40, 64) == 0 and ws(5, 1 << 20) == 0
+
+
+def test_norm_binding_refuses_before_the_library_is_called():
+    m, _ = _lib()
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(64, dtype=torch.bfloat16)
+    for bad in (x, None, x[0]):
+        with pytest.raises(TypeError):
+            m.mx_rmsnorm(bad, w)                               # not on a GPU, not a matrix
+        with pytest.raises(TypeError):
+            m.mx_rmsnorm_backward(bad, x, w, torch.zeros(4))
+
+
+def _runtime(name):
+    out = subprocess.run(["g++", f"-print-file-name={name}"], capture_output=True, text=True).stdout.strip()
+    return out if os.path.isabs(out) and os.path.exists(out) else None
+
+
+def test_validation_under_asan_and_ubsan():
+    """The host code built with g++ as a host-only library whose launchers are stubs; this file reruns against it
+    with the sanitizer runtime preloaded.  No GPU code is built or run."""
+    if os.environ.get("MXQ_TEST_SANITIZED_LIBRARY"):
+        pytest.skip("inner run")
+    rocm = "/opt/rocm"
+    if shutil.which("g++") is None or not os.path.isdir(os.path.join(rocm, "include", "hip")):
+        pytest.skip("needs g++ and the ROCm headers")
+    asan = _runtime("libasan.so")
+    if asan is None:
+        pytest.skip("libasan not found")
+    tmp = tempfile.mkdtemp(prefix="mxq_asan_")
+    try:
+        lib = os.path.join(tmp, "libmxq_host_asan.so")
+        csrc = os.path.join(ROOT, "microscaling_quantization_block_amd", "csrc")
+        san = os.path.join(ROOT, "tests", "sanitize")
+        build = ["g++", "-std=c++17", "-O1", "-g", "-fPIC", "-shared", "-fsanitize=address,undefined",
+                 "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer", "-D__HIP_PLATFORM_AMD__",
+                 "-I", os.path.join(rocm, "include"), "-I", os.path.join(ROOT, "include"), "-I", csrc]
+        build += [os.path.join(csrc, f) for f in ("api.cpp", "api_decode.cpp", "api_layer.cpp")]
+        build += [os.path.join(san, f) for f in ("host_stubs.cpp", "host_stubs_decode.cpp", "host_stubs_layer.cpp")]
+        build += ["-L", os.path.join(rocm, "lib"), "-lamdhip64", f"-Wl,-rpath,{os.path.join(rocm, 'lib')}", "-o", lib]
+        r = subprocess.run(build, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr[-3000:]
+        env = dict(os.environ)
+        env.update(LD_PRELOAD=asan, MXQ_TEST_SANITIZED_LIBRARY=lib,
+                   ASAN_OPTIONS="detect_leaks=0:detect_odr_violation=0:halt_on_error=1:abort_on_error=0",
+                   UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+        r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-p", "no:cacheprovider",
+                            os.path.join(ROOT, "tests", "test_layer_abi.py")],
+                           cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
+        report = r.stdout[-4000:] + r.stderr[-4000:]
+        assert r.returncode == 0, report
+        assert "passed" in r.stdout and "ERROR: AddressSanitizer" not in report and "runtime error" not in report
+    finally:
+        shutil.rmtree(tmp, ignore_errors=True)
