@@ -1,7 +1,8 @@
 /*
  * mxq_layer.h -- the steps of a decoder layer around its quantized products:
  * the root-mean-square norm with the residual's addition and a quantized
- * output, and its gradient.
+ * output, the router of a layer with experts, the rows of its tokens ordered by
+ * expert and back, each with its gradient.
  * Included by mxq.h; the conventions there hold for every entry (caller-owned
  * device memory, work enqueued on the caller's stream, host validation before
  * any launch, no allocation, no exception).
@@ -73,6 +74,81 @@ mxq_status mx_rmsnorm_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t
                                int64_t ld_dr, int64_t rows, int64_t cols, uint16_t* dx, int64_t ld_dx,
                                float* dweight, void* workspace, int64_t workspace_bytes, void* stream);
 int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+
+/*
+ * The rows of a layer with experts.  Token t uses the experts
+ * experts[t, 0 .. topk - 1]; each such slot has one row in the experts' products,
+ * and the rows are ordered by (expert, token, slot):
+ *   offsets    [num_experts + 1]: expert e has the rows [offsets[e], offsets[e+1])
+ *              (group_row_offsets of mx_gemm, mx_gemm_swiglu, nvfp4_gemv ...)
+ *   row_token  [tokens * topk]: the token of every row (a_row_index, x_row_index);
+ *              0 from row offsets[num_experts] on, rows that no expert has
+ *   row_of     [tokens, topk]: the row of every slot, -1 for a slot without one
+ * A slot whose expert is outside [0, num_experts) has no row: experts that are on
+ * another device, or none.
+ *
+ * mx_moe_sort -- these three from given ids, experts int32 [tokens, topk].
+ *
+ * mx_moe_route -- the router: experts[t] are the topk largest logits of token t,
+ * largest first, ties to the lower expert, and weights[t] their softmax
+ * probabilities: over the chosen experts (renormalize) or over all of them.  An
+ * expert whose logit is -infinity is never chosen: its slot has the id -1, the weight 0 and no
+ * row.  A NaN counts as the largest logit, and makes its token's weights NaN,
+ * as an infinity does.  Then the rows as mx_moe_sort orders them.
+ *   logits       binary32 (logits_f32) or BF16 [tokens, num_experts], row stride ld
+ *   experts      int32 [tokens, topk], weights binary32 [tokens, topk]: outputs
+ *   workspace    device, 16-byte aligned, mx_moe_workspace() bytes (may be NULL if
+ *                that is 0); calls in flight at once need one each
+ *
+ * mx_moe_route_backward -- dlogits [tokens, num_experts] (type of the logits, row stride ld_d)
+ * from dweights [tokens, topk] and what mx_moe_route gave; the choice itself
+ * has no gradient.
+ *
+ * Sizes: num_experts up to 1024, topk up to 64 and num_experts; tokens below
+ * 2^24, tokens * topk up to 2^26.  tokens == 0 gives offsets of zeros.
+ */
+mxq_status mx_moe_route(const void* logits, int32_t logits_f32, int64_t ld, int64_t tokens, int32_t num_experts,
+                        int32_t topk, int32_t renormalize, int32_t* experts, float* weights, int32_t* offsets,
+                        int32_t* row_token, int32_t* row_of, void* workspace, int64_t workspace_bytes, void* stream);
+mxq_status mx_moe_route_backward(const float* dweights, const void* logits, int32_t logits_f32, int64_t ld,
+                                 int64_t tokens, int32_t num_experts, int32_t topk, int32_t renormalize,
+                                 const int32_t* experts, const float* weights, void* dlogits, int64_t ld_d,
+                                 void* stream);
+mxq_status mx_moe_sort(const int32_t* experts, int64_t tokens, int32_t num_experts, int32_t topk, int32_t* offsets,
+                       int32_t* row_token, int32_t* row_of, void* workspace, int64_t workspace_bytes, void* stream);
+int64_t mx_moe_workspace(int64_t tokens, int32_t num_experts, int32_t topk);
+
+/*
+ * Tokens to the experts' rows and back, by row_of int32 [tokens, topk].  An entry
+ * outside [0, num_rows) has no row: nothing is read or written for it.  Rows that no
+ * entry names are left as they were.  Each row belongs to one entry (as
+ * mx_moe_sort makes them); where two entries of mx_moe_dispatch or
+ * mx_moe_combine_backward name one row, either is left there, or a mixture.
+ *
+ * mx_moe_dispatch -- rows[row_of[t, j]] = x[t], BF16.  (The products gather by row_token
+ * themselves; this is for what needs the rows in memory, as the columnwise copy of
+ * a weight gradient.)  Its gradient is mx_moe_combine of the rows' gradients with weights NULL.
+ *
+ * mx_moe_combine -- out[t] = sum over j of weights[t, j] rows[row_of[t, j]], in
+ * binary32 in the order of j, one rounding to BF16; weights NULL: ones.  A token
+ * without rows gives zeros.
+ *
+ * mx_moe_combine_backward -- the gradient of mx_moe_combine:
+ *   drows[row_of[t, j]] = weights[t, j] dout[t]      (BF16)
+ *   dweights[t, j]      = dout[t] . rows[row_of[t, j]]  (binary32; 0 without a row)
+ *
+ * Matrices are BF16 with row strides in elements; cols % 8 == 0, 16-byte
+ * alignment, strides multiples of 8.  Sizes as mx_moe_sort; cols below 2^26.
+ */
+mxq_status mx_moe_dispatch(const uint16_t* x, int64_t ld_x, int64_t tokens, int64_t cols, const int32_t* row_of,
+                           int32_t topk, uint16_t* rows, int64_t ld_rows, int64_t num_rows, void* stream);
+mxq_status mx_moe_combine(const uint16_t* rows, int64_t ld_rows, int64_t num_rows, const int32_t* row_of,
+                          const float* weights, int64_t tokens, int64_t cols, int32_t topk, uint16_t* out,
+                          int64_t ld_out, void* stream);
+mxq_status mx_moe_combine_backward(const uint16_t* dout, int64_t ld_dout, const uint16_t* rows, int64_t ld_rows,
+                                   int64_t num_rows, const int32_t* row_of, const float* weights, int64_t tokens,
+                                   int64_t cols, int32_t topk, uint16_t* drows, int64_t ld_drows, float* dweights,
+                                   void* stream);
 
 #ifdef __cplusplus
 }

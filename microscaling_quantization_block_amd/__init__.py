@@ -9,7 +9,8 @@ and, for the decode step (decode.py, include/mxq_decode.h):
     nvfp4_gemv, nvfp4_gemv_swiglu, NVFP4Cache, nvfp4_cache_append,
     nvfp4_attention
 and, for the steps around a layer's products (layer.py, include/mxq_layer.h):
-    mx_rmsnorm, mx_rmsnorm_backward
+    mx_rmsnorm, mx_rmsnorm_backward, mx_moe_route, mx_moe_route_backward,
+    mx_moe_sort, mx_moe_dispatch, mx_moe_combine, mx_moe_combine_backward
 Outputs the caller does not pass are allocated here with torch (the library
 itself never allocates).  Every call is asynchronous on the current stream.
 
@@ -30,7 +31,9 @@ __all__ = ["Format", "Block", "GScale", "Round", "Layout", "Operand", "MXQError"
            "mx_swiglu", "mx_gemm_set_tile", "library_path", "lib",
            "NVFP4Cache", "nvfp4_gemv", "nvfp4_gemv_swiglu", "nvfp4_cache_append", "nvfp4_attention",
            "nvfp4_attention_workspace",
-           "RMSNorm", "mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace"]
+           "RMSNorm", "mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace",
+           "MoERows", "MoERouting", "mx_moe_route", "mx_moe_route_backward", "mx_moe_sort", "mx_moe_workspace",
+           "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libmxq.so")
@@ -522,4 +525,6 @@ def mx_gemm_set_tile(tile):
 
 from .decode import (NVFP4Cache, nvfp4_attention, nvfp4_attention_workspace,  # noqa: E402
                      nvfp4_cache_append, nvfp4_gemv, nvfp4_gemv_swiglu)
-from .layer import RMSNorm, mx_rmsnorm, mx_rmsnorm_backward, mx_rmsnorm_backward_workspace  # noqa: E402
+from .layer import (MoERouting, MoERows, RMSNorm, mx_moe_combine, mx_moe_combine_backward,  # noqa: E402
+                    mx_moe_dispatch, mx_moe_route, mx_moe_route_backward, mx_moe_sort, mx_moe_workspace, mx_rmsnorm,
+                    mx_rmsnorm_backward, mx_rmsnorm_backward_workspace)

@@ -36,6 +36,66 @@ mxq_status check_norm_shape(const char* fn, int64_t rows, int64_t cols) {
   return MXQ_OK;
 }
 
+// Sizes of the experts' rows.
+mxq_status check_slots(const char* fn, int64_t tokens, int topk) {
+  if (tokens < 0) return fail(MXQ_EINVAL, "%s: negative size", fn);
+  if (topk < 1 || topk > mxq::MOE_TOPK) return fail(MXQ_EINVAL, "%s: topk must be 1 to %d (topk=%d)", fn, mxq::MOE_TOPK, topk);
+  if (tokens >= (1 << 24) || tokens * topk > (1 << 26))
+    return fail(MXQ_EUNSUPPORTED, "%s: too many tokens for one call (below 2^24, 2^26 slots)", fn);
+  return MXQ_OK;
+}
+
+mxq_status check_experts(const char* fn, int64_t tokens, int num_experts, int topk) {
+  const mxq_status s = check_slots(fn, tokens, topk);
+  if (s != MXQ_OK) return s;
+  if (num_experts < 1) return fail(MXQ_EINVAL, "%s: no experts", fn);
+  if (num_experts > mxq::MOE_EXPERTS)
+    return fail(MXQ_EUNSUPPORTED, "%s: up to %d experts (num_experts=%d)", fn, mxq::MOE_EXPERTS, num_experts);
+  if (topk > num_experts) return fail(MXQ_ESHAPE, "%s: topk exceeds the experts (%d, %d)", fn, topk, num_experts);
+  return MXQ_OK;
+}
+
+mxq_status check_logits(const char* fn, const char* name, const void* p, bool f32, int64_t ld, int num_experts) {
+  if (!p) return fail(MXQ_EINVAL, "%s: %s is NULL", fn, name);
+  if (ld < num_experts) return fail(MXQ_EINVAL, "%s: leading dimension of %s smaller than the row", fn, name);
+  if (ld >= I31) return fail(MXQ_EUNSUPPORTED, "%s: leading dimension of %s too large", fn, name);
+  if (!aligned(p, f32 ? 4 : 2)) return fail(MXQ_EALIGN, "%s: %s is not aligned to its type", fn, name);
+  return MXQ_OK;
+}
+
+// The outputs of the sort, its workspace and its plan.
+mxq_status check_sort(const char* fn, mxq::MoeArgs& a, bool routed, void* workspace, int64_t workspace_bytes) {
+  if (!a.offsets) return fail(MXQ_EINVAL, "%s: offsets is NULL", fn);
+  if (a.T > 0 && (!a.experts || !a.row_token || !a.row_of)) return fail(MXQ_EINVAL, "%s: null pointer", fn);
+  if (!aligned(a.offsets, 4) || !aligned(a.experts, 4) || !aligned(a.row_token, 4) || !aligned(a.row_of, 4) ||
+      !aligned(a.weights, 4))
+    return fail(MXQ_EALIGN, "%s: arrays 4-byte aligned", fn);
+  mxq::plan_moe(a, routed);
+  const int64_t need = a.groups * mxq::moe_pad(a.E) * 2;
+  if (need) {
+    if (!workspace || workspace_bytes < need)
+      return fail(MXQ_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)need);
+    if (!aligned16(workspace)) return fail(MXQ_EALIGN, "%s: workspace 16-byte aligned", fn);
+    a.counts = static_cast<uint16_t*>(workspace);
+  }
+  return MXQ_OK;
+}
+
+// Sizes, row_of and the matrices of a call on the experts' rows.  Sets nothing to do where there is nothing.
+mxq_status check_rows_call(const char* fn, const mxq::MoeRowsArgs& a) {
+  const mxq_status s = check_slots(fn, a.T, a.k);
+  if (s != MXQ_OK) return s;
+  if (a.cols < 0 || a.M < 0) return fail(MXQ_EINVAL, "%s: negative size", fn);
+  if (a.cols % 8) return fail(MXQ_ESHAPE, "%s: cols %% 8 == 0 (cols=%lld)", fn, (long long)a.cols);
+  if (a.cols >= (1 << 26)) return fail(MXQ_EUNSUPPORTED, "%s: cols below 2^26", fn);
+  if (a.M >= I31) return fail(MXQ_EUNSUPPORTED, "%s: too many rows", fn);
+  if (a.T == 0) return MXQ_OK;
+  if (!a.row_of) return fail(MXQ_EINVAL, "%s: row_of is NULL", fn);
+  if (!aligned(a.row_of, 4) || !aligned(a.weights, 4) || !aligned(a.dweights, 4))
+    return fail(MXQ_EALIGN, "%s: arrays 4-byte aligned", fn);
+  return MXQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,6 +212,169 @@ mxq_status mx_rmsnorm_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t
   a.dw = dweight;
   a.part = static_cast<float*>(workspace);
   return hip_status(mxq::launch_rmsnorm_backward(a, S(stream)), fn);
+}
+
+int64_t mx_moe_workspace(int64_t tokens, int32_t num_experts, int32_t topk) {
+  if (tokens <= 0 || tokens >= (1 << 24) || topk < 1 || topk > mxq::MOE_TOPK || num_experts < 1 ||
+      num_experts > mxq::MOE_EXPERTS)
+    return 0;                                  // nothing to do, or refused
+  mxq::MoeArgs a = {};
+  a.T = tokens;
+  a.k = topk;
+  int64_t groups = 0;
+  for (const bool routed : {false, true}) {
+    mxq::plan_moe(a, routed);
+    if (a.groups > groups) groups = a.groups;
+  }
+  return groups * mxq::moe_pad(num_experts) * 2;
+}
+
+mxq_status mx_moe_route(const void* logits, int32_t logits_f32, int64_t ld, int64_t tokens, int32_t num_experts,
+                        int32_t topk, int32_t renormalize, int32_t* experts, float* weights, int32_t* offsets,
+                        int32_t* row_token, int32_t* row_of, void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* fn = "mx_moe_route";
+  mxq_status s = check_experts(fn, tokens, num_experts, topk);
+  if (s != MXQ_OK) return s;
+  if (tokens > 0) {
+    if ((s = check_logits(fn, "logits", logits, logits_f32, ld, num_experts)) != MXQ_OK) return s;
+    if (!weights) return fail(MXQ_EINVAL, "%s: weights is NULL", fn);
+  }
+  mxq::MoeArgs a = {};
+  a.logits = logits;
+  a.f32 = logits_f32 != 0;
+  a.renorm = renormalize != 0;
+  a.ld = ld;
+  a.T = tokens;
+  a.E = num_experts;
+  a.k = topk;
+  a.experts = experts;
+  a.weights = weights;
+  a.offsets = offsets;
+  a.row_token = row_token;
+  a.row_of = row_of;
+  if ((s = check_sort(fn, a, true, workspace, workspace_bytes)) != MXQ_OK) return s;
+  return hip_status(mxq::launch_moe_route(a, S(stream)), fn);
+}
+
+mxq_status mx_moe_sort(const int32_t* experts, int64_t tokens, int32_t num_experts, int32_t topk, int32_t* offsets,
+                       int32_t* row_token, int32_t* row_of, void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* fn = "mx_moe_sort";
+  mxq_status s = check_experts(fn, tokens, num_experts, 1);
+  if (s != MXQ_OK || (s = check_slots(fn, tokens, topk)) != MXQ_OK) return s;
+  mxq::MoeArgs a = {};
+  a.T = tokens;
+  a.E = num_experts;
+  a.k = topk;
+  a.experts = const_cast<int32_t*>(experts);   // read only
+  a.offsets = offsets;
+  a.row_token = row_token;
+  a.row_of = row_of;
+  if ((s = check_sort(fn, a, false, workspace, workspace_bytes)) != MXQ_OK) return s;
+  return hip_status(mxq::launch_moe_sort(a, S(stream)), fn);
+}
+
+mxq_status mx_moe_route_backward(const float* dweights, const void* logits, int32_t logits_f32, int64_t ld,
+                                 int64_t tokens, int32_t num_experts, int32_t topk, int32_t renormalize,
+                                 const int32_t* experts, const float* weights, void* dlogits, int64_t ld_d,
+                                 void* stream) {
+  const char* fn = "mx_moe_route_backward";
+  mxq_status s = check_experts(fn, tokens, num_experts, topk);
+  if (s != MXQ_OK) return s;
+  if (tokens == 0) return ok();
+  if ((s = check_logits(fn, "logits", logits, logits_f32, ld, num_experts)) != MXQ_OK) return s;
+  if ((s = check_logits(fn, "dlogits", dlogits, logits_f32, ld_d, num_experts)) != MXQ_OK) return s;
+  if (!dweights || !experts || !weights) return fail(MXQ_EINVAL, "%s: null pointer", fn);
+  if (!aligned(dweights, 4) || !aligned(experts, 4) || !aligned(weights, 4))
+    return fail(MXQ_EALIGN, "%s: arrays 4-byte aligned", fn);
+  mxq::RouteBwdArgs a = {};
+  a.dweights = dweights;
+  a.logits = logits;
+  a.f32 = logits_f32 != 0;
+  a.renorm = renormalize != 0;
+  a.ld = ld;
+  a.T = tokens;
+  a.E = num_experts;
+  a.k = topk;
+  a.experts = experts;
+  a.weights = weights;
+  a.dlogits = dlogits;
+  a.ld_d = ld_d;
+  return hip_status(mxq::launch_moe_route_backward(a, S(stream)), fn);
+}
+
+mxq_status mx_moe_dispatch(const uint16_t* x, int64_t ld_x, int64_t tokens, int64_t cols, const int32_t* row_of,
+                           int32_t topk, uint16_t* rows, int64_t ld_rows, int64_t num_rows, void* stream) {
+  const char* fn = "mx_moe_dispatch";
+  mxq::MoeRowsArgs a = {};
+  a.T = tokens;
+  a.cols = cols;
+  a.M = num_rows;
+  a.k = topk;
+  a.row_of = row_of;
+  a.x = x;
+  a.ld_x = ld_x;
+  a.to_rows = rows;
+  a.ld_to = ld_rows;
+  mxq_status s = check_rows_call(fn, a);
+  if (s != MXQ_OK) return s;
+  if (tokens == 0 || cols == 0 || num_rows == 0) return ok();
+  if ((s = check_matrix(fn, "x", x, ld_x, cols)) != MXQ_OK) return s;
+  if ((s = check_matrix(fn, "rows", rows, ld_rows, cols)) != MXQ_OK) return s;
+  return hip_status(mxq::launch_moe_dispatch(a, S(stream)), fn);
+}
+
+mxq_status mx_moe_combine(const uint16_t* rows, int64_t ld_rows, int64_t num_rows, const int32_t* row_of,
+                          const float* weights, int64_t tokens, int64_t cols, int32_t topk, uint16_t* out,
+                          int64_t ld_out, void* stream) {
+  const char* fn = "mx_moe_combine";
+  mxq::MoeRowsArgs a = {};
+  a.T = tokens;
+  a.cols = cols;
+  a.M = num_rows;
+  a.k = topk;
+  a.row_of = row_of;
+  a.weights = weights;
+  a.rows = rows;
+  a.ld_rows = ld_rows;
+  a.out = out;
+  a.ld_out = ld_out;
+  mxq_status s = check_rows_call(fn, a);
+  if (s != MXQ_OK) return s;
+  if (tokens == 0 || cols == 0) return ok();
+  if (num_rows > 0 && (s = check_matrix(fn, "rows", rows, ld_rows, cols)) != MXQ_OK) return s;
+  if ((s = check_matrix(fn, "out", out, ld_out, cols)) != MXQ_OK) return s;
+  return hip_status(mxq::launch_moe_combine(a, S(stream)), fn);
+}
+
+mxq_status mx_moe_combine_backward(const uint16_t* dout, int64_t ld_dout, const uint16_t* rows, int64_t ld_rows,
+                                   int64_t num_rows, const int32_t* row_of, const float* weights, int64_t tokens,
+                                   int64_t cols, int32_t topk, uint16_t* drows, int64_t ld_drows, float* dweights,
+                                   void* stream) {
+  const char* fn = "mx_moe_combine_backward";
+  mxq::MoeRowsArgs a = {};
+  a.T = tokens;
+  a.cols = cols;
+  a.M = num_rows;
+  a.k = topk;
+  a.row_of = row_of;
+  a.weights = weights;
+  a.x = dout;
+  a.ld_x = ld_dout;
+  a.rows = rows;
+  a.ld_rows = ld_rows;
+  a.to_rows = drows;
+  a.ld_to = ld_drows;
+  a.dweights = dweights;
+  mxq_status s = check_rows_call(fn, a);
+  if (s != MXQ_OK) return s;
+  if (tokens == 0) return ok();
+  if (!weights || !dweights) return fail(MXQ_EINVAL, "%s: null pointer", fn);
+  if (cols > 0 && num_rows > 0) {
+    if ((s = check_matrix(fn, "dout", dout, ld_dout, cols)) != MXQ_OK) return s;
+    if ((s = check_matrix(fn, "rows", rows, ld_rows, cols)) != MXQ_OK) return s;
+    if ((s = check_matrix(fn, "drows", drows, ld_drows, cols)) != MXQ_OK) return s;
+  }
+  return hip_status(mxq::launch_moe_combine_backward(a, S(stream)), fn);
 }
 
 }  // extern "C"

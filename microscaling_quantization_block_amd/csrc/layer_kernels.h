@@ -44,4 +44,56 @@ struct NormBwdArgs {
 int64_t norm_bwd_groups(int64_t rows, int64_t cols);
 hipError_t launch_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st);
 
+// Rows of the experts: ids [T, k] to rows ordered by (expert, token).
+struct MoeArgs {
+  const void* logits;           // [T, E], binary32 or BF16 (mx_moe_route)
+  int f32, renorm;
+  int64_t ld;
+  int64_t T;
+  int E, k;
+  int32_t* experts;             // [T, k]: written by the router, else given
+  float* weights;               // [T, k]
+  int32_t *offsets;             // [E + 1]
+  int32_t *row_token, *row_of;  // [T k], [T, k]
+  uint16_t* counts;             // [groups, moe_pad(E)] tokens' slots of each expert
+  int64_t groups, group_tokens;
+};
+constexpr int MOE_EXPERTS = 1024, MOE_TOPK = 64;
+// Experts of a row of counts: whole 16-byte loads.
+inline int64_t moe_pad(int E) { return (E + 7) / 8 * 8; }
+// Sets a.groups (0: one workgroup does it all, without counts) and a.group_tokens.
+void plan_moe(MoeArgs& a, bool routed);
+hipError_t launch_moe_route(const MoeArgs& a, hipStream_t st);
+hipError_t launch_moe_sort(const MoeArgs& a, hipStream_t st);
+
+struct RouteBwdArgs {
+  const float* dweights;        // [T, k]
+  const void* logits;
+  int f32, renorm;
+  int64_t ld, T;
+  int E, k;
+  const int32_t* experts;
+  const float* weights;
+  void* dlogits;                // as logits
+  int64_t ld_d;
+};
+hipError_t launch_moe_route_backward(const RouteBwdArgs& a, hipStream_t st);
+
+struct MoeRowsArgs {
+  int64_t T, cols, M;           // tokens, values of a row, rows of the experts
+  int k;
+  const int32_t* row_of;        // [T, k]
+  const float* weights;         // [T, k], or nullptr: ones
+  const uint16_t* x;            // tokens' rows in
+  uint16_t* out;                // tokens' rows out
+  int64_t ld_x, ld_out;
+  const uint16_t* rows;         // experts' rows in
+  uint16_t* to_rows;            // experts' rows out
+  int64_t ld_rows, ld_to;
+  float* dweights;              // [T, k]
+};
+hipError_t launch_moe_dispatch(const MoeRowsArgs& a, hipStream_t st);
+hipError_t launch_moe_combine(const MoeRowsArgs& a, hipStream_t st);
+hipError_t launch_moe_combine_backward(const MoeRowsArgs& a, hipStream_t st);
+
 }  // namespace mxq

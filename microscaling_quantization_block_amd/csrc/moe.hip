@@ -1,0 +1,520 @@
+// The router of a layer with experts, the rows of its tokens ordered by expert,
+// and the way there and back with its gradients.
+//
+// Router: a token's k largest logits, ties to the lower expert, and their softmax weights
+// (over the chosen ones, or over all experts).  A token is 16 lanes or a wave, expert
+// v LANES + lane in lane; a round finds the largest key by lane exchanges, then the lowest
+// expert that has it, and takes it out.
+//
+// Order: rows by (expert, token, slot), a counting sort.  Each group of tokens
+// counts its slots by expert; a second kernel adds the counts of the groups before its own
+// and of the experts before each, and gives every slot its row: lanes with the same
+// expert rank themselves by ballots over the bits of the expert's number, so that no
+// order depends on the timing of atomics.  Few tokens are routed and sorted by one workgroup in one launch.
+//
+// There and back: a lane owns eight columns; all of a token's rows are in flight
+// at once, so these are copies bound by memory.
+
+#include "lanes.h"
+#include "layer_kernels.h"
+
+#include <type_traits>
+
+namespace mxq {
+
+namespace {
+
+// Binary32 values as unsigned integers of the same order.  Both zeros give one
+// key, a NaN the largest; 0 stands for an expert that is not there (any more).
+constexpr uint32_t KEY_MINUS_INF = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t key_of(float x) {
+  if (x != x) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);      // 0xFFFFFFFF: a NaN
+}
+
+__device__ __forceinline__ float logit(const void* logits, int f32, int64_t i) {
+  if (f32) return static_cast<const float*>(logits)[i];
+  return __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[i] << 16);
+}
+
+constexpr int SORT_WAVES = 8;
+
+// Routes token t (LANES lanes, `lane` of them); counts its experts in hist.
+template <int LANES, int VPL>
+__device__ __forceinline__ void route_token(const MoeArgs& a, int64_t t, int lane, int* hist) {
+  uint32_t key[VPL];
+  uint32_t top = 0;
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const int e = v * LANES + lane;
+    key[v] = e < a.E ? key_of(logit(a.logits, a.f32, t * a.ld + e)) : 0u;
+    top = umax(top, key[v]);
+  }
+  top = lanes_max<LANES>(top);
+  const float largest = value_of(top);
+  float all = 0.0f;
+  if (!a.renorm) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      if (key[v]) all += expf(value_of(key[v]) - largest);
+    all = lanes_sum<LANES>(all);
+  }
+  int mine = -1;                               // lane j: the expert of slot j and its key
+  uint32_t mine_key = 0;
+  for (int j = 0; j < a.k; ++j) {
+    if (j) {
+      top = 0;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) top = umax(top, key[v]);
+      top = lanes_max<LANES>(top);
+    }
+    if (top <= KEY_MINUS_INF) break;           // nothing is left for this token
+    uint32_t low = 0;                          // ~expert: the largest is the lowest expert
+#pragma unroll
+    for (int v = VPL - 1; v >= 0; --v) low = key[v] == top ? ~(uint32_t)(v * LANES + lane) : low;
+    const int e = (int)~lanes_max<LANES>(low);
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) key[v] = v * LANES + lane == e ? 0u : key[v];
+    if (lane == j) {
+      mine = e;
+      mine_key = top;
+    }
+  }
+  const float part = mine >= 0 ? expf(value_of(mine_key) - largest) : 0.0f;
+  const float total = a.renorm ? lanes_sum<LANES>(part) : all;
+  if (lane < a.k) {
+    a.experts[t * a.k + lane] = mine;
+    a.weights[t * a.k + lane] = mine >= 0 ? part / total : 0.0f;
+    if (mine >= 0) atomicAdd(&hist[mine], 1);
+  }
+}
+
+// The number that goes before n counts of the workgroup's threads in turn: an
+// exclusive sum over threads.  `scratch` holds an int per wave.
+template <int THREADS>
+__device__ __forceinline__ int block_exclusive_sum(int n, int* scratch) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int s = n;
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const int up = __shfl_up(s, o, 64);
+    if (lane >= o) s += up;
+  }
+  if (lane == 63) scratch[wave] = s;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < wave; ++i) before += scratch[i];
+  return before + s - n;
+}
+
+// LDS of the sort: hist [SORT_WAVES, E], then total and before [E] each.
+inline size_t sort_lds(int E) { return (size_t)(SORT_WAVES + 2) * E * 4; }
+
+// Gives the slots [first, last) of the call (this workgroup's) their rows.
+// GROUPS: their counts and those of the other groups are in a.counts; else they are all there is.
+template <int THREADS, bool GROUPS>
+__device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int64_t first, int64_t last, int* lds) {
+  __shared__ int scratch[THREADS / 64];
+  __shared__ int all_rows;
+  const int E = a.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int* hist = lds;
+  int* total = lds + SORT_WAVES * E;
+  int* before = total + E;
+  for (int i = threadIdx.x; i < (SORT_WAVES + 2) * E; i += THREADS) lds[i] = 0;
+  __syncthreads();
+  // whole 64-slot pieces of the workgroup's slots, in order, to the waves in order
+  const int64_t pieces = (last - first + 63) / 64, each = (pieces + SORT_WAVES - 1) / SORT_WAVES;
+  const int64_t from = first + wave * each * 64, to = min(last, from + each * 64);
+  if (wave < SORT_WAVES)
+    for (int64_t s = from + lane; s < to; s += 64) {
+      const int e = a.experts[s];
+      if ((unsigned)e < (unsigned)E) atomicAdd(&hist[wave * E + e], 1);
+    }
+  if constexpr (GROUPS) {
+    // a lane adds eight experts' counts over every (THREADS / lanes of a row)-th group
+    const int per_row = (E + 7) / 8, slices = THREADS / per_row;
+    const int c = threadIdx.x % per_row, slice = threadIdx.x / per_row;
+    int sum[8], pre[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = pre[i] = 0;
+    if (slice < slices) {
+#pragma unroll 4
+      for (int64_t g = slice; g < a.groups; g += slices) {
+        const uint4 w = *reinterpret_cast<const uint4*>(a.counts + (g * per_row + c) * 8);
+        const uint32_t n[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int lo = (int)(n[i] & 0xFFFFu), hi = (int)(n[i] >> 16);
+          sum[2 * i] += lo;
+          sum[2 * i + 1] += hi;
+          pre[2 * i] += g < group ? lo : 0;
+          pre[2 * i + 1] += g < group ? hi : 0;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c * 8 + i < E) {
+          atomicAdd(&total[c * 8 + i], sum[i]);
+          atomicAdd(&before[c * 8 + i], pre[i]);
+        }
+    }
+    __syncthreads();
+  } else {
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += THREADS) {
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < SORT_WAVES; ++w) n += hist[w * E + e];
+      total[e] = n;
+    }
+    __syncthreads();
+  }
+  // the experts' first rows, then those of this workgroup's waves
+  const int per = (E + THREADS - 1) / THREADS, e0 = min(E, (int)threadIdx.x * per), e1 = min(E, e0 + per);
+  int n = 0;
+  for (int e = e0; e < e1; ++e) n += total[e];
+  int start = block_exclusive_sum<THREADS>(n, scratch);
+  for (int e = e0; e < e1; ++e) {
+    if (group == 0) a.offsets[e] = start;
+    int at = start + before[e];
+#pragma unroll
+    for (int w = 0; w < SORT_WAVES; ++w) {
+      const int m = hist[w * E + e];
+      hist[w * E + e] = at;
+      at += m;
+    }
+    start += total[e];
+  }
+  if (threadIdx.x == THREADS - 1) {            // the last thread's end is the sum of all
+    if (group == 0) a.offsets[E] = start;
+    all_rows = start;
+  }
+  __syncthreads();
+  const int64_t rows = all_rows;
+  const int bits = 32 - __clz(E);              // of numbers up to E, which stands for no expert
+  if (wave < SORT_WAVES)
+    for (int64_t s0 = from; s0 < to; s0 += 64) {
+      const int64_t s = s0 + lane;
+      int e = s < to ? a.experts[s] : E;
+      e = (unsigned)e < (unsigned)E ? e : E;
+      uint64_t same = ~0ull;                   // lanes with this expert
+      for (int b = 0; b < bits; ++b) {
+        const bool one = (e >> b) & 1;
+        const uint64_t ones = __ballot(one);
+        same &= one ? ones : ~ones;
+      }
+      const int leader = __ffsll((unsigned long long)same) - 1;
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      int at = 0;
+      if (lane == leader && e < E) at = atomicAdd(&hist[wave * E + e], __popcll(same));
+      at = __shfl(at, leader, 64) + rank;
+      // the next piece's counts come after this one's
+      __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+      if (s < to) {
+        a.row_of[s] = e < E ? at : -1;
+        if (e < E) a.row_token[at] = (int)(s / a.k);
+      }
+    }
+  // rows of no slot: token 0, a row that a gather may read
+  for (int64_t r = first + threadIdx.x; r < last; r += THREADS)
+    if (r >= rows) a.row_token[r] = 0;
+}
+
+template <int LANES, int VPL>
+__global__ __launch_bounds__(256) void route_kernel(MoeArgs a) {
+  extern __shared__ int lds[];
+  for (int i = threadIdx.x; i < a.E; i += 256) lds[i] = 0;
+  __syncthreads();
+  const int64_t first = blockIdx.x * a.group_tokens, last = min(a.T, first + a.group_tokens);
+  for (int64_t t = first + threadIdx.x / LANES; t < last; t += 256 / LANES)
+    route_token<LANES, VPL>(a, t, threadIdx.x & (LANES - 1), lds);
+  __syncthreads();
+  const int pad = (a.E + 7) / 8 * 8;
+  for (int i = threadIdx.x; i < pad; i += 256) a.counts[blockIdx.x * (int64_t)pad + i] = (uint16_t)(i < a.E ? lds[i] : 0);
+}
+
+template <int LANES, int VPL>
+__global__ __launch_bounds__(1024) void route_one_kernel(MoeArgs a) {
+  extern __shared__ int lds[];
+  for (int64_t t = threadIdx.x / LANES; t < a.T; t += 1024 / LANES)
+    route_token<LANES, VPL>(a, t, threadIdx.x & (LANES - 1), lds);     // its counts are not used
+  __syncthreads();
+  sort_slots<1024, false>(a, 0, 0, a.T * a.k, lds);
+}
+
+__global__ __launch_bounds__(256) void count_kernel(MoeArgs a) {
+  extern __shared__ int lds[];
+  for (int i = threadIdx.x; i < a.E; i += 256) lds[i] = 0;
+  __syncthreads();
+  const int64_t first = blockIdx.x * a.group_tokens * a.k, last = min(a.T * a.k, first + a.group_tokens * a.k);
+  for (int64_t s = first + threadIdx.x; s < last; s += 256) {
+    const int e = a.experts[s];
+    if ((unsigned)e < (unsigned)a.E) atomicAdd(&lds[e], 1);
+  }
+  __syncthreads();
+  const int pad = (a.E + 7) / 8 * 8;
+  for (int i = threadIdx.x; i < pad; i += 256) a.counts[blockIdx.x * (int64_t)pad + i] = (uint16_t)(i < a.E ? lds[i] : 0);
+}
+
+__global__ __launch_bounds__(512) void sort_kernel(MoeArgs a) {
+  extern __shared__ int lds[];
+  const int64_t slots = a.T * a.k, each = a.group_tokens * a.k, first = blockIdx.x * each;
+  sort_slots<512, true>(a, blockIdx.x, first, min(slots, first + each), lds);
+}
+
+__global__ __launch_bounds__(1024) void sort_one_kernel(MoeArgs a) {
+  extern __shared__ int lds[];
+  sort_slots<1024, false>(a, 0, 0, a.T * a.k, lds);
+}
+
+// dl of the softmax: over the chosen experts w_j (dw_j - sum w dw); over all of
+// them p_e (dw_e - sum w dw), dw_e 0 where e was not chosen.
+template <int LANES, int VPL>
+__global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
+  const int lane = threadIdx.x & (LANES - 1);
+  const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  if (t >= a.T) return;                        // whole groups of LANES lanes leave
+  const int32_t* ids = a.experts + t * a.k;
+  const float *w = a.weights + t * a.k, *dw = a.dweights + t * a.k;
+  float mean = 0.0f;
+  for (int j = 0; j < a.k; ++j)
+    if (ids[j] >= 0) mean = __builtin_fmaf(w[j], dw[j], mean);
+  float d[VPL];
+  if (a.renorm) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) d[v] = 0.0f;
+  } else {
+    float x[VPL], top = -__builtin_inff(), total = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int e = v * LANES + lane;
+      x[v] = e < a.E ? logit(a.logits, a.f32, t * a.ld + e) : -__builtin_inff();
+      top = fmaxf(top, x[v]);
+    }
+    top = value_of(lanes_max<LANES>(key_of(top)));
+    // a token whose experts are all masked has weights of zero: nothing flows
+    const float base = top > -__builtin_inff() ? top : 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      x[v] = expf(x[v] - base);
+      total += x[v];
+    }
+    total = lanes_sum<LANES>(total);
+    const float r = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) d[v] = -(x[v] * r) * mean;
+  }
+  for (int j = 0; j < a.k; ++j) {
+    const int e = ids[j];
+    const float g = w[j] * (a.renorm ? dw[j] - mean : dw[j]);
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) d[v] += e == v * LANES + lane ? g : 0.0f;
+  }
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const int e = v * LANES + lane;
+    if (e >= a.E) continue;
+    if (a.f32) static_cast<float*>(a.dlogits)[t * a.ld_d + e] = d[v];
+    else static_cast<uint16_t*>(a.dlogits)[t * a.ld_d + e] = (uint16_t)f32x2_to_bf16x2(d[v], 0.0f);
+  }
+}
+
+// Calls f<LANES, VPL>() for E experts and k choices: 16 lanes a token up to 256 experts (four tokens a wave: for 128
+// experts a round is 50 instructions for all four), a wave beyond, and where 16 lanes cannot hold the choices.
+template <class F>
+hipError_t with_lanes(int E, int k, F&& f) {
+  if (k <= 16) {
+    if (E <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
+    if (E <= 64) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
+    if (E <= 128) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 8>());
+    if (E <= 256) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
+  }
+  if (E <= 256) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
+  if (E <= 512) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
+  return f(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
+}
+
+}  // namespace
+
+void plan_moe(MoeArgs& a, bool routed) {
+  a.groups = 0;
+  a.group_tokens = a.T;
+  // one workgroup routes 64 tokens in a pass, or sorts a few thousand slots
+  if (routed ? a.T <= 64 : a.T * a.k <= 4096) return;
+  // 32 tokens a workgroup of the router are two passes; up to 256 groups beyond that, while counts fit 16 bits
+  int64_t each = (a.T + 255) / 256;
+  each = each < 32 ? 32 : each;
+  const int64_t most = 65535 / a.k;
+  a.group_tokens = each < most ? each : most;
+  a.groups = (a.T + a.group_tokens - 1) / a.group_tokens;
+}
+
+hipError_t launch_moe_route(const MoeArgs& a, hipStream_t st) {
+  const hipError_t e = with_lanes(a.E, a.k, [&](auto lanes, auto vpl) {
+    constexpr int LANES = decltype(lanes)::value, VPL = decltype(vpl)::value;
+    if (!a.groups)
+      hipLaunchKernelGGL((route_one_kernel<LANES, VPL>), dim3(1), dim3(1024), sort_lds(a.E), st, a);
+    else
+      hipLaunchKernelGGL((route_kernel<LANES, VPL>), dim3((unsigned)a.groups), dim3(256), (size_t)a.E * 4, st, a);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || !a.groups) return e;
+  hipLaunchKernelGGL(sort_kernel, dim3((unsigned)a.groups), dim3(512), sort_lds(a.E), st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_sort(const MoeArgs& a, hipStream_t st) {
+  if (!a.groups) {
+    hipLaunchKernelGGL(sort_one_kernel, dim3(1), dim3(1024), sort_lds(a.E), st, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(count_kernel, dim3((unsigned)a.groups), dim3(256), (size_t)a.E * 4, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(sort_kernel, dim3((unsigned)a.groups), dim3(512), sort_lds(a.E), st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_route_backward(const RouteBwdArgs& a, hipStream_t st) {
+  return with_lanes(a.E, a.k, [&](auto lanes, auto vpl) {
+    constexpr int LANES = decltype(lanes)::value, VPL = decltype(vpl)::value;
+    const int64_t grid = (a.T + 256 / LANES - 1) / (256 / LANES);
+    hipLaunchKernelGGL((route_backward_kernel<LANES, VPL>), dim3((unsigned)grid), dim3(256), 0, st, a);
+    return hipGetLastError();
+  });
+}
+
+// ---------------------------------------------------------- there and back
+
+namespace {
+
+__device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void store16(uint16_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
+
+// 2^lx lanes hold 8 2^lx columns of a token; 256 / 2^lx tokens a workgroup.
+struct Place {
+  int64_t t, c;                                // token, first column
+  bool there;
+};
+__device__ __forceinline__ Place place_of(const MoeRowsArgs& a, int lx) {
+  Place p;
+  p.t = (int64_t)blockIdx.x * (256 >> lx) + (threadIdx.x >> lx);
+  p.c = (((int64_t)blockIdx.y << lx) + (threadIdx.x & ((1 << lx) - 1))) * 8;
+  p.there = p.t < a.T && p.c < a.cols;
+  return p;
+}
+
+__global__ __launch_bounds__(256) void dispatch_kernel(MoeRowsArgs a, int lx) {
+  const Place p = place_of(a, lx);
+  if (!p.there) return;
+  const uint4 v = load16(a.x + p.t * a.ld_x + p.c);
+  const int32_t* row_of = a.row_of + p.t * a.k;
+  for (int j = 0; j < a.k; ++j) {
+    const int64_t r = row_of[j];
+    if (r >= 0 && r < a.M) store16(a.to_rows + r * a.ld_to + p.c, v);
+  }
+}
+
+__global__ __launch_bounds__(256) void combine_kernel(MoeRowsArgs a, int lx) {
+  const Place p = place_of(a, lx);
+  if (!p.there) return;
+  const int32_t* row_of = a.row_of + p.t * a.k;
+  const float* weights = a.weights ? a.weights + p.t * a.k : nullptr;
+  float sum[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+  constexpr int B = 8;                         // rows in flight
+  for (int j0 = 0; j0 < a.k; j0 += B) {
+    uint4 v[B];
+    float w[B];
+    bool has[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      has[j] = false;
+      if (j0 + j < a.k) {
+        const int64_t r = row_of[j0 + j];
+        has[j] = r >= 0 && r < a.M;
+        w[j] = weights ? weights[j0 + j] : 1.0f;
+        if (has[j]) v[j] = load16(a.rows + r * a.ld_rows + p.c);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+      if (has[j]) {
+        const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[2 * i] = __builtin_fmaf(w[j], bf16_lo(u[i]), sum[2 * i]);
+          sum[2 * i + 1] = __builtin_fmaf(w[j], bf16_hi(u[i]), sum[2 * i + 1]);
+        }
+      }
+  }
+  store16(a.out + p.t * a.ld_out + p.c, make_uint4(f32x2_to_bf16x2(sum[0], sum[1]), f32x2_to_bf16x2(sum[2], sum[3]),
+                                                   f32x2_to_bf16x2(sum[4], sum[5]), f32x2_to_bf16x2(sum[6], sum[7])));
+}
+
+// A wave per slot: drow = w dout, dw = dout . row.
+__global__ __launch_bounds__(256) void combine_backward_kernel(MoeRowsArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t s = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (s >= a.T * a.k) return;                  // whole waves leave
+  const int64_t t = s / a.k, r = a.row_of[s];
+  if (r < 0 || r >= a.M) {                     // no row, no gradient
+    if (lane == 0) a.dweights[s] = 0.0f;
+    return;
+  }
+  const float w = a.weights[s];
+  const uint16_t *g = a.x + t * a.ld_x, *y = a.rows + r * a.ld_rows;
+  uint16_t* d = a.to_rows + r * a.ld_to;
+  float dot = 0.0f;
+#pragma unroll 4
+  for (int64_t c = 8 * lane; c < a.cols; c += 512) {
+    const uint4 gv = load16(g + c), yv = load16(y + c);
+    const uint32_t gu[4] = {gv.x, gv.y, gv.z, gv.w}, yu[4] = {yv.x, yv.y, yv.z, yv.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dot = __builtin_fmaf(bf16_lo(gu[i]), bf16_lo(yu[i]), dot);
+      dot = __builtin_fmaf(bf16_hi(gu[i]), bf16_hi(yu[i]), dot);
+      o[i] = f32x2_to_bf16x2(w * bf16_lo(gu[i]), w * bf16_hi(gu[i]));
+    }
+    store16(d + c, make_uint4(o[0], o[1], o[2], o[3]));
+  }
+  dot = lanes_sum<64>(dot);
+  if (lane == 0) a.dweights[s] = dot;
+}
+
+int lanes_log2(int64_t cols) {
+  int lx = 0;
+  while (lx < 8 && (int64_t)8 << lx < cols) ++lx;
+  return lx;
+}
+dim3 rows_grid(const MoeRowsArgs& a, int lx) {
+  const int64_t tokens = 256 >> lx, cols = (int64_t)8 << lx;
+  return dim3((unsigned)((a.T + tokens - 1) / tokens), (unsigned)((a.cols + cols - 1) / cols));
+}
+
+}  // namespace
+
+hipError_t launch_moe_dispatch(const MoeRowsArgs& a, hipStream_t st) {
+  const int lx = lanes_log2(a.cols);
+  hipLaunchKernelGGL(dispatch_kernel, rows_grid(a, lx), dim3(256), 0, st, a, lx);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const MoeRowsArgs& a, hipStream_t st) {
+  const int lx = lanes_log2(a.cols);
+  hipLaunchKernelGGL(combine_kernel, rows_grid(a, lx), dim3(256), 0, st, a, lx);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_backward(const MoeRowsArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL(combine_backward_kernel, dim3((unsigned)((a.T * a.k + 3) / 4)), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace mxq

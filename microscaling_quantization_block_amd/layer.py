@@ -1,5 +1,6 @@
 """Binding of the steps around a layer's products (include/mxq_layer.h): the
-root-mean-square norm with a quantized output, and its gradient.
+root-mean-square norm with a quantized output, the router of a layer with
+experts, the rows of its tokens ordered by expert and back, each with its gradient.
 
 Like decode.py: argument marshalling and host checks only, outputs and
 workspaces the caller does not pass are allocated with torch, and every call is
@@ -14,7 +15,9 @@ import torch
 from . import Format, Layout, lib
 from .decode import _check_tensor, _launch, _p, _takes_stream
 
-__all__ = ["RMSNorm", "mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace"]
+__all__ = ["RMSNorm", "mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace",
+           "MoERows", "MoERouting", "mx_moe_route", "mx_moe_route_backward", "mx_moe_sort", "mx_moe_workspace",
+           "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward"]
 
 _fns = None
 
@@ -28,9 +31,18 @@ def _lib():
                                  i64, vp]
         L.mx_rmsnorm_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, vp, i64, vp, vp, i64, vp]
         L.mx_rmsnorm_backward_workspace.argtypes = [i64, i64]
-        for f in ("mx_rmsnorm", "mx_rmsnorm_backward"):
+        L.mx_moe_route.argtypes = [vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, i64, vp]
+        L.mx_moe_route_backward.argtypes = [vp, vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, i64, vp]
+        L.mx_moe_sort.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, i64, vp]
+        L.mx_moe_workspace.argtypes = [i64, i32, i32]
+        L.mx_moe_dispatch.argtypes = [vp, i64, i64, i64, vp, i32, vp, i64, i64, vp]
+        L.mx_moe_combine.argtypes = [vp, i64, i64, vp, vp, i64, i64, i32, vp, i64, vp]
+        L.mx_moe_combine_backward.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, i64, i32, vp, i64, vp, vp]
+        for f in ("mx_rmsnorm", "mx_rmsnorm_backward", "mx_moe_route", "mx_moe_route_backward", "mx_moe_sort",
+                  "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward"):
             getattr(L, f).restype = ctypes.c_int
-        L.mx_rmsnorm_backward_workspace.restype = i64
+        for f in ("mx_rmsnorm_backward_workspace", "mx_moe_workspace"):
+            getattr(L, f).restype = i64
         _fns = L
     return _fns
 
@@ -164,3 +176,166 @@ def mx_rmsnorm_backward(dy, h, weight, rstd, dresidual=None, dx=None, dweight=No
     _launch(dev, _lib().mx_rmsnorm_backward, dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, weight.data_ptr(), rstd.data_ptr(),
             _p(dresidual), ld_dr, rows, cols, dx.data_ptr(), ld_dx, _p(dweight), _p(workspace), have)
     return dx, dweight
+
+
+# ------------------------------------------------------------ the experts' rows
+
+class MoERows(NamedTuple):
+    """Rows ordered by (expert, token): int32 offsets [experts + 1], the token of every row [tokens * topk] and the row
+    of every slot [tokens, topk] (-1: none)."""
+    offsets: torch.Tensor
+    row_token: torch.Tensor
+    row_of: torch.Tensor
+
+
+class MoERouting(NamedTuple):
+    """A router's choice: int32 experts and float32 weights [tokens, topk], and the rows as in MoERows."""
+    experts: torch.Tensor
+    weights: torch.Tensor
+    offsets: torch.Tensor
+    row_token: torch.Tensor
+    row_of: torch.Tensor
+
+
+def _rows_out(T, E, k, dev, offsets, row_token, row_of):
+    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device=dev)
+    offsets = i32(E + 1) if offsets is None else offsets
+    row_token = i32(T * k) if row_token is None else row_token
+    row_of = i32(T, k) if row_of is None else row_of
+    for t, name, n in ((offsets, "offsets", E + 1), (row_token, "row_token", T * k), (row_of, "row_of", T * k)):
+        _flat(t, name, torch.int32, n, dev)
+    return offsets, row_token, row_of
+
+
+def _workspace(need, workspace, dev):
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=dev), need) if need else (None, 0)
+    _check_tensor(workspace, "workspace", torch.uint8, 1, dev)
+    return workspace, workspace.numel() if workspace.is_contiguous() else 0
+
+
+def _logits(t, name, T, E, dev):
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return _matrix(t, name, T, E, dev, t.dtype)
+
+
+def mx_moe_workspace(tokens, num_experts, topk):
+    """Bytes of workspace that mx_moe_route and mx_moe_sort need for these sizes; may be 0."""
+    return _lib().mx_moe_workspace(tokens, num_experts, topk)
+
+
+@_takes_stream
+def mx_moe_route(logits, topk, renormalize=True, experts=None, weights=None, offsets=None, row_token=None, row_of=None,
+                 workspace=None):
+    """The router: the topk largest of the float32 or BF16 logits [tokens,
+    experts] of every token (ties to the lower expert, -inf never chosen), their
+    softmax weights (over the chosen ones, or over all experts without
+    renormalize), and the tokens' rows ordered by expert.  Returns a MoERouting:
+    offsets and row_token go to the grouped products as group_row_offsets and
+    a_row_index or x_row_index, row_of and weights to mx_moe_combine."""
+    T, E, dev = _first(logits, "logits")
+    ld = _logits(logits, "logits", T, E, dev)
+    experts = torch.empty((T, topk), dtype=torch.int32, device=dev) if experts is None else experts
+    weights = torch.empty((T, topk), dtype=torch.float32, device=dev) if weights is None else weights
+    _flat(experts, "experts", torch.int32, T * topk, dev)
+    _flat(weights, "weights", torch.float32, T * topk, dev)
+    offsets, row_token, row_of = _rows_out(T, E, topk, dev, offsets, row_token, row_of)
+    workspace, have = _workspace(_lib().mx_moe_workspace(T, E, topk), workspace, dev)
+    _launch(dev, _lib().mx_moe_route, logits.data_ptr(), logits.dtype is torch.float32, ld, T, E, topk, bool(renormalize),
+            experts.data_ptr(), weights.data_ptr(), offsets.data_ptr(), row_token.data_ptr(), row_of.data_ptr(),
+            _p(workspace), have)
+    return MoERouting(experts, weights, offsets, row_token, row_of)
+
+
+@_takes_stream
+def mx_moe_route_backward(dweights, logits, experts, weights, renormalize=True, dlogits=None):
+    """Gradient of mx_moe_route's weights: dlogits like the logits, from float32
+    dweights [tokens, topk] and what the forward call took and gave."""
+    T, E, dev = _first(logits, "logits")
+    ld = _logits(logits, "logits", T, E, dev)
+    if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
+        raise TypeError("experts must be a 2-D int32 tensor")
+    k = experts.shape[1]
+    _flat(experts, "experts", torch.int32, T * k, dev)
+    for t, name in ((weights, "weights"), (dweights, "dweights")):
+        _flat(t, name, torch.float32, T * k, dev)
+    dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev) if dlogits is None else dlogits
+    ld_d = _matrix(dlogits, "dlogits", T, E, dev, logits.dtype)
+    _launch(dev, _lib().mx_moe_route_backward, dweights.data_ptr(), logits.data_ptr(), logits.dtype is torch.float32, ld, T,
+            E, k, bool(renormalize), experts.data_ptr(), weights.data_ptr(), dlogits.data_ptr(), ld_d)
+    return dlogits
+
+
+@_takes_stream
+def mx_moe_sort(experts, num_experts, offsets=None, row_token=None, row_of=None, workspace=None):
+    """The rows of given int32 expert ids [tokens, topk], ordered by (expert,
+    token): a MoERows.  An id outside [0, num_experts) has no row."""
+    T, k, dev = _first(experts, "experts")
+    _flat(experts, "experts", torch.int32, T * k, dev)
+    offsets, row_token, row_of = _rows_out(T, num_experts, k, dev, offsets, row_token, row_of)
+    workspace, have = _workspace(_lib().mx_moe_workspace(T, num_experts, k), workspace, dev)
+    _launch(dev, _lib().mx_moe_sort, experts.data_ptr(), T, num_experts, k, offsets.data_ptr(), row_token.data_ptr(),
+            row_of.data_ptr(), _p(workspace), have)
+    return MoERows(offsets, row_token, row_of)
+
+
+def _row_of(row_of, T, dev):
+    if not isinstance(row_of, torch.Tensor) or row_of.dim() != 2:
+        raise TypeError("row_of must be a 2-D int32 tensor")
+    k = row_of.shape[1]
+    _flat(row_of, "row_of", torch.int32, (row_of.shape[0] if T is None else T) * k, dev)
+    return row_of.shape[0], k
+
+
+@_takes_stream
+def mx_moe_dispatch(x, row_of, num_rows=None, out=None):
+    """rows[row_of[t, j]] = x[t] for the BF16 rows x [tokens, cols]: the experts'
+    rows [num_rows, cols] in memory (num_rows: tokens * topk).  Rows that no
+    slot names are left as they were.  Its gradient is mx_moe_combine(drows, row_of)."""
+    T, cols, dev = _first(x, "x")
+    ld_x = _matrix(x, "x", T, cols, dev)
+    _, k = _row_of(row_of, T, dev)
+    if num_rows is None:
+        num_rows = T * k if out is None else out.shape[0]
+    out = torch.empty((num_rows, cols), dtype=torch.bfloat16, device=dev) if out is None else out
+    ld_out = _matrix(out, "out", num_rows, cols, dev)
+    _launch(dev, _lib().mx_moe_dispatch, x.data_ptr(), ld_x, T, cols, row_of.data_ptr(), k, out.data_ptr(), ld_out, num_rows)
+    return out
+
+
+@_takes_stream
+def mx_moe_combine(rows, row_of, weights=None, out=None):
+    """out[t] = sum over j of weights[t, j] rows[row_of[t, j]] (ones without
+    weights): the experts' BF16 rows back to [tokens, cols], summed in float32.  A
+    token without rows gives zeros."""
+    M, cols, dev = _first(rows, "rows")
+    ld_rows = _matrix(rows, "rows", M, cols, dev)
+    T, k = _row_of(row_of, None, dev)
+    if weights is not None:
+        _flat(weights, "weights", torch.float32, T * k, dev)
+    out = torch.empty((T, cols), dtype=torch.bfloat16, device=dev) if out is None else out
+    ld_out = _matrix(out, "out", T, cols, dev)
+    _launch(dev, _lib().mx_moe_combine, rows.data_ptr(), ld_rows, M, row_of.data_ptr(), _p(weights), T, cols, k,
+            out.data_ptr(), ld_out)
+    return out
+
+
+@_takes_stream
+def mx_moe_combine_backward(dout, rows, row_of, weights, drows=None, dweights=None):
+    """Gradient of mx_moe_combine: (drows like rows, dweights float32 [tokens,
+    topk]) from dout [tokens, cols].  Rows of drows that no slot names are left
+    as they were."""
+    T, cols, dev = _first(dout, "dout")
+    ld_d = _matrix(dout, "dout", T, cols, dev)
+    M = rows.shape[0] if isinstance(rows, torch.Tensor) and rows.dim() else 0
+    ld_rows = _matrix(rows, "rows", M, cols, dev)
+    _, k = _row_of(row_of, T, dev)
+    _flat(weights, "weights", torch.float32, T * k, dev)
+    drows = torch.empty((M, cols), dtype=torch.bfloat16, device=dev) if drows is None else drows
+    ld_dr = _matrix(drows, "drows", M, cols, dev)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=dev) if dweights is None else dweights
+    _flat(dweights, "dweights", torch.float32, T * k, dev)
+    _launch(dev, _lib().mx_moe_combine_backward, dout.data_ptr(), ld_d, rows.data_ptr(), ld_rows, M, row_of.data_ptr(),
+            weights.data_ptr(), T, cols, k, drows.data_ptr(), ld_dr, dweights.data_ptr())
+    return drows, dweights

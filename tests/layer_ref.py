@@ -53,3 +53,76 @@ def norm_backward_ref(dy, h, w, rstd, dres=None):
     dw = (dy * xhat).sum(0)
     ew = (h.shape[0] + 4) * 2 * EPS_F32 * np.abs(dy * xhat).sum(0)
     return dx, dw, EPS_BF16 * np.abs(dx) + (1 + EPS_BF16) * e + TINY_BF16, ew
+
+
+# ------------------------------------------------------------ the experts' rows
+
+def route_ref(x, k, renorm):
+    """experts [T, k] (-1: none), weights [T, k] in float64 and their bound, from logits x [T, E] (float64).
+
+    A weight is exp(d) over a sum, d = x - max: binary32 rounds d (d 2^-24 on the exponential), the exponential (four
+    half steps), each of the n additions and the quotient."""
+    T, E = x.shape
+    order = np.where(np.isnan(x), np.inf, x)
+    # NaN before +inf, then by value, then by index
+    place = np.lexsort((np.broadcast_to(np.arange(E), x.shape), -order, ~np.isnan(x)), axis=1)[:, :k]
+    top = np.take_along_axis(x, place, 1)
+    chosen = ~(top == -np.inf)
+    with np.errstate(all="ignore"):
+        d = top - top[:, :1]
+        p = np.exp(d)
+        total = np.where(chosen, p, 0).sum(1) if renorm else np.exp(x - top[:, :1]).sum(1)
+        w = np.where(chosen, p / total[:, None], 0.0)
+        spread = np.where(chosen, np.abs(d), 0).max(1)[:, None] if renorm else np.abs(
+            np.where(x > -np.inf, x - top[:, :1], 0)).max(1)[:, None]
+        tol = np.where(chosen, w * (2 * spread + 2 * E + 16) * EPS_F32 + 2.0 ** -148, 0.0)
+    return np.where(chosen, place, -1).astype(np.int32), w, tol
+
+
+def rows_ref(ids, E):
+    """offsets, row_token, row_of of ids [T, k]: rows by (expert, token, slot)."""
+    T, k = ids.shape
+    flat = ids.reshape(-1).astype(np.int64)
+    key = np.where((flat < 0) | (flat >= E), E, flat)
+    order = np.argsort(key, kind="stable")
+    counts = np.bincount(key, minlength=E + 1)[:E]
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    n = int(offsets[-1])
+    row_token, row_of = np.zeros(T * k, np.int32), np.full(T * k, -1, np.int32)
+    row_token[:n] = order[:n] // k
+    row_of[order[:n]] = np.arange(n)
+    return offsets, row_token, row_of.reshape(T, k)
+
+
+def route_backward_ref(dw, x, ids, w, renorm):
+    """dlogits in float64 (weights w in float64) and a bound: w is off by its own bound, which is passed on."""
+    T, E = x.shape
+    has = ids >= 0
+    mean = np.where(has, w * dw, 0).sum(1)[:, None]
+    d = np.zeros((T, E))
+    size = np.zeros((T, E))
+    if not renorm:
+        with np.errstate(all="ignore"):
+            p = np.exp(x - x.max(1, keepdims=True))
+            p = np.nan_to_num(p / p.sum(1, keepdims=True))
+        d = -p * mean
+        size = p * np.where(has, w * np.abs(dw), 0).sum(1)[:, None]
+    for t in range(T):
+        for j in range(ids.shape[1]):
+            if has[t, j]:
+                d[t, ids[t, j]] += w[t, j] * (dw[t, j] - mean[t, 0] if renorm else dw[t, j])
+                size[t, ids[t, j]] += w[t, j] * (np.abs(dw[t, j]) + np.where(has[t], w[t] * np.abs(dw[t]), 0).sum())
+    spread = np.where(np.isfinite(x), np.abs(x - x.max(1, keepdims=True)), 0).max(1, keepdims=True)
+    return d, size * (4 * spread + 4 * E + 64) * EPS_F32 + 2.0 ** -140
+
+
+def combine_ref(rows, row_of, weights):
+    """out [T, cols] in float64 and its bound."""
+    T, k = row_of.shape
+    ok = (row_of >= 0) & (row_of < rows.shape[0])
+    y = np.where(ok[..., None], rows[np.where(ok, row_of, 0)], 0.0)
+    w = np.ones((T, k)) if weights is None else weights
+    t = y * w[..., None]
+    out = t.sum(1)
+    e = (k + 1) * 2 * EPS_F32 * np.abs(t).sum(1)
+    return out, EPS_BF16 * np.abs(out) + (1 + EPS_BF16) * e + TINY_BF16

@@ -18,7 +18,8 @@ from tests.util import ROOT
 FAKE = ctypes.c_void_p(0x10000)       # never dereferenced: validation fails first
 ODD = ctypes.c_void_p(0x10008)
 EINVAL, ESHAPE, EALIGN, EUNSUPPORTED = 1, 2, 3, 4
-NAMES = ["mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace"]
+NAMES = ["mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace", "mx_moe_route", "mx_moe_route_backward",
+         "mx_moe_sort", "mx_moe_workspace", "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward"]
 
 
 def _lib():
@@ -106,6 +107,95 @@ def test_norm_binding_refuses_before_the_library_is_called():
             m.mx_rmsnorm(bad, w)                               # not on a GPU, not a matrix
         with pytest.raises(TypeError):
             m.mx_rmsnorm_backward(bad, x, w, torch.zeros(4))
+
+
+def test_route_and_sort_reject_bad_arguments():
+    m, L = _lib()
+    big, two = 1 << 40, ctypes.c_void_p(0x10002)
+
+    def route(x=FAKE, f32=1, ld=16, T=100, E=16, k=4, renorm=1, ids=FAKE, w=FAKE, off=FAKE, tok=FAKE, row=FAKE, ws=FAKE,
+              n=big):
+        return L.mx_moe_route(x, f32, ld, T, E, k, renorm, ids, w, off, tok, row, ws, n, None)
+
+    def sort(ids=FAKE, T=5000, E=16, k=4, off=FAKE, tok=FAKE, row=FAKE, ws=FAKE, n=big):
+        return L.mx_moe_sort(ids, T, E, k, off, tok, row, ws, n, None)
+
+    for kw in (dict(x=None), dict(w=None), dict(ids=None), dict(off=None), dict(tok=None), dict(row=None), dict(T=-1),
+               dict(E=0), dict(k=0), dict(k=65, E=100, ld=100), dict(ld=15), dict(ws=None), dict(n=127)):
+        assert route(**kw) == EINVAL, kw
+    for kw in (dict(ids=None), dict(off=None), dict(tok=None), dict(row=None), dict(T=-1), dict(E=0), dict(k=0), dict(k=65),
+               dict(ws=None), dict(n=100)):
+        assert sort(**kw) == EINVAL, kw
+        assert "mx_moe_sort" in m.lib().mxq_last_error().decode()
+    assert route(k=17) == ESHAPE
+    for kw in (dict(x=two), dict(f32=0, x=ctypes.c_void_p(0x10001)), dict(w=two), dict(ids=two), dict(off=two), dict(ws=ODD)):
+        assert route(**kw) == EALIGN, kw
+    for kw in (dict(ids=two), dict(tok=two), dict(row=two), dict(ws=ODD)):
+        assert sort(**kw) == EALIGN, kw
+    for kw in (dict(E=1025, ld=1025), dict(T=1 << 24), dict(T=(1 << 24) - 1, k=5), dict(ld=1 << 31)):
+        assert route(**kw) == EUNSUPPORTED, kw
+    for kw in (dict(E=1025), dict(T=1 << 24), dict(T=(1 << 24) - 1, k=5)):
+        assert sort(**kw) == EUNSUPPORTED, kw
+    ws = m.mx_moe_workspace
+    assert ws(0, 16, 4) == 0 and ws(1, 16, 4) == 0 and ws(100, 16, 4) > 0 and ws(-1, 16, 4) == 0 and ws(1 << 30, 16, 4) == 0
+    assert ws(100, 0, 4) == 0 and ws(100, 16, 0) == 0 and ws(100, 1 << 20, 4) == 0
+
+
+def test_route_backward_rejects_bad_arguments():
+    m, L = _lib()
+    two = ctypes.c_void_p(0x10002)
+
+    def call(dw=FAKE, x=FAKE, f32=1, ld=16, T=9, E=16, k=4, ids=FAKE, w=FAKE, d=FAKE, ld_d=16):
+        return L.mx_moe_route_backward(dw, x, f32, ld, T, E, k, 1, ids, w, d, ld_d, None)
+
+    for kw in (dict(dw=None), dict(x=None), dict(ids=None), dict(w=None), dict(d=None), dict(ld=15), dict(ld_d=15),
+               dict(T=-1), dict(E=0), dict(k=0)):
+        assert call(**kw) == EINVAL, kw
+    for kw in (dict(dw=two), dict(x=two), dict(ids=two), dict(w=two), dict(d=two)):
+        assert call(**kw) == EALIGN, kw
+    assert call(k=17) == ESHAPE and call(E=2000, ld=2000, ld_d=2000) == EUNSUPPORTED and call(T=0, x=None) == 0
+
+
+def test_rows_calls_reject_bad_arguments():
+    m, L = _lib()
+    two = ctypes.c_void_p(0x10002)
+
+    def dispatch(x=FAKE, ld=64, T=5, cols=64, row=FAKE, k=2, rows=FAKE, ld_r=64, M=10):
+        return L.mx_moe_dispatch(x, ld, T, cols, row, k, rows, ld_r, M, None)
+
+    def combine(rows=FAKE, ld_r=64, M=10, row=FAKE, w=FAKE, T=5, cols=64, k=2, out=FAKE, ld=64):
+        return L.mx_moe_combine(rows, ld_r, M, row, w, T, cols, k, out, ld, None)
+
+    def backward(g=FAKE, ld=64, rows=FAKE, ld_r=64, M=10, row=FAKE, w=FAKE, T=5, cols=64, k=2, dr=FAKE, ld_dr=64, dw=FAKE):
+        return L.mx_moe_combine_backward(g, ld, rows, ld_r, M, row, w, T, cols, k, dr, ld_dr, dw, None)
+
+    for fn in (dispatch, combine, backward):
+        for kw in (dict(row=None), dict(rows=None), dict(T=-1), dict(cols=-8), dict(k=0), dict(k=65), dict(M=-1), dict(ld=56),
+                   dict(ld_r=56)):
+            assert fn(**kw) == EINVAL, (fn, kw)
+        for kw in (dict(rows=ODD), dict(ld=68), dict(ld_r=68), dict(row=two)):
+            assert fn(**kw) == EALIGN, (fn, kw)
+        assert fn(cols=60) == ESHAPE
+        for kw in (dict(T=1 << 24), dict(T=(1 << 24) - 1, k=5), dict(cols=1 << 26, ld=1 << 26, ld_r=1 << 26),
+                   dict(M=1 << 31)):
+            assert fn(**kw) == EUNSUPPORTED, (fn, kw)
+        assert fn(T=0, row=None) == 0
+    assert dispatch(x=None) == EINVAL and combine(out=None) == EINVAL and dispatch(x=ODD) == EALIGN
+    for kw in (dict(g=None), dict(w=None), dict(dr=None), dict(dw=None), dict(ld_dr=56)):
+        assert backward(**kw) == EINVAL, kw
+    for kw in (dict(g=ODD), dict(dr=ODD), dict(w=two), dict(dw=two), dict(ld_dr=68)):
+        assert backward(**kw) == EALIGN, kw
+    assert combine(w=two) == EALIGN and dispatch(M=0) == 0 and dispatch(cols=0) == 0
+
+
+def test_moe_binding_refuses_before_the_library_is_called():
+    m, _ = _lib()
+    x, i = torch.zeros(4, 64), torch.zeros(4, 2, dtype=torch.int32)
+    for call in (lambda: m.mx_moe_route(x, 2), lambda: m.mx_moe_sort(i, 4), lambda: m.mx_moe_dispatch(x, i),
+                 lambda: m.mx_moe_combine(x, i), lambda: m.mx_moe_combine_backward(x, x, i, x),
+                 lambda: m.mx_moe_route_backward(x, x, i, x), lambda: m.mx_moe_route(None, 2)):
+        with pytest.raises(TypeError):
+            call()                                             # not on a GPU
 
 
 def _runtime(name):
