@@ -2,7 +2,8 @@
  * mxq_layer.h -- the steps of a decoder layer around its quantized products:
  * the root-mean-square norm with the residual's addition and a quantized
  * output, the router of a layer with experts, the rows of its tokens ordered by
- * expert and back, each with its gradient.
+ * expert and back, each with its gradient; rotary positions on the way into the
+ * NVFP4 cache.
  * Included by mxq.h; the conventions there hold for every entry (caller-owned
  * device memory, work enqueued on the caller's stream, host validation before
  * any launch, no allocation, no exception).
@@ -149,6 +150,34 @@ mxq_status mx_moe_combine_backward(const uint16_t* dout, int64_t ld_dout, const 
                                    int64_t num_rows, const int32_t* row_of, const float* weights, int64_t tokens,
                                    int64_t cols, int32_t topk, uint16_t* drows, int64_t ld_drows, float* dweights,
                                    void* stream);
+
+/*
+ * nvfp4_rope_append -- rotary positions for the call's rows q and k, and k and
+ * v quantized into the cache as nvfp4_cache_append does it.  The requests, the
+ * cache, k, v, k_dq and v_dq are those of nvfp4_cache_append; a row at position
+ * p (seq_lens[b] - rows + i, as there) has the first rotary_dim values of every q
+ * and k head turned by the angles p inv_freq[i], i < rotary_dim / 2:
+ *   (a, b) -> (a c - b s, b c + a s),  c = fl(factor cos), s = fl(factor sin)
+ * where (a, b) are the values (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with
+ * `interleaved`.  Cosine and sine are taken in binary64, the products and their
+ * sum in binary32, and the turned row is rounded to BF16: q_out gets it, and the
+ * cache the bytes of nvfp4_cache_append for the turned k.  Positions scaled for
+ * long contexts are other frequencies (and a factor).
+ *   q, q_out      BF16 [tokens, num_q_heads, head_dim], strides in elements
+ *                 (multiples of 8), head_dim contiguous, 16-byte aligned; q_out
+ *                 may be q itself, with its strides.  Rows of no request are not written.
+ *   inv_freq      binary32 [rotary_dim / 2], on the device; p inv_freq[i] below 2^40
+ *   rotary_dim    a multiple of 16, up to head_dim
+ * Any positive num_q_heads: q and the cache need not belong to one attention.
+ */
+mxq_status nvfp4_rope_append(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int32_t num_q_heads,
+                             const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
+                             int64_t v_token_stride, int64_t v_head_stride, int64_t tokens, const mxq_cache* cache,
+                             const int32_t* block_table, int64_t ld_table, int64_t table_width,
+                             const int32_t* seq_lens, const int32_t* q_offsets, int64_t num_requests,
+                             const float* inv_freq, int32_t rotary_dim, int32_t interleaved, double factor,
+                             uint16_t* q_out, int64_t out_token_stride, int64_t out_head_stride, uint16_t* k_dq,
+                             uint16_t* v_dq, void* stream);
 
 #ifdef __cplusplus
 }

@@ -10,7 +10,8 @@ and, for the decode step (decode.py, include/mxq_decode.h):
     nvfp4_attention
 and, for the steps around a layer's products (layer.py, include/mxq_layer.h):
     mx_rmsnorm, mx_rmsnorm_backward, mx_moe_route, mx_moe_route_backward,
-    mx_moe_sort, mx_moe_dispatch, mx_moe_combine, mx_moe_combine_backward
+    mx_moe_sort, mx_moe_dispatch, mx_moe_combine, mx_moe_combine_backward,
+    nvfp4_rope_append
 Outputs the caller does not pass are allocated here with torch (the library
 itself never allocates).  Every call is asynchronous on the current stream.
 
@@ -33,7 +34,7 @@ __all__ = ["Format", "Block", "GScale", "Round", "Layout", "Operand", "MXQError"
            "nvfp4_attention_workspace",
            "RMSNorm", "mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace",
            "MoERows", "MoERouting", "mx_moe_route", "mx_moe_route_backward", "mx_moe_sort", "mx_moe_workspace",
-           "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward"]
+           "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward", "nvfp4_rope_append"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libmxq.so")
@@ -527,4 +528,4 @@ from .decode import (NVFP4Cache, nvfp4_attention, nvfp4_attention_workspace,  # 
                      nvfp4_cache_append, nvfp4_gemv, nvfp4_gemv_swiglu)
 from .layer import (MoERouting, MoERows, RMSNorm, mx_moe_combine, mx_moe_combine_backward,  # noqa: E402
                     mx_moe_dispatch, mx_moe_route, mx_moe_route_backward, mx_moe_sort, mx_moe_workspace, mx_rmsnorm,
-                    mx_rmsnorm_backward, mx_rmsnorm_backward_workspace)
+                    mx_rmsnorm_backward, mx_rmsnorm_backward_workspace, nvfp4_rope_append)

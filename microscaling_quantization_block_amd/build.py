@@ -22,7 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmxq.so")
 SOURCES = ["api.cpp", "quant_mxfp8.hip", "quant_nvfp4.hip", "dequant.hip", "gemm.hip", "gemm_fp8s.hip",
-           "api_decode.cpp", "gemv.hip", "cache.hip", "attention.hip", "api_layer.cpp", "norm.hip", "moe.hip"]
+           "api_decode.cpp", "gemv.hip", "cache.hip", "attention.hip", "api_layer.cpp", "norm.hip", "moe.hip",
+           "rope.hip"]
 
 
 def hipcc():

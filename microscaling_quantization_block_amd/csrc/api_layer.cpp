@@ -377,4 +377,54 @@ mxq_status mx_moe_combine_backward(const uint16_t* dout, int64_t ld_dout, const 
   return hip_status(mxq::launch_moe_combine_backward(a, S(stream)), fn);
 }
 
+mxq_status nvfp4_rope_append(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int32_t num_q_heads,
+                             const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
+                             int64_t v_token_stride, int64_t v_head_stride, int64_t tokens, const mxq_cache* cache,
+                             const int32_t* block_table, int64_t ld_table, int64_t table_width,
+                             const int32_t* seq_lens, const int32_t* q_offsets, int64_t num_requests,
+                             const float* inv_freq, int32_t rotary_dim, int32_t interleaved, double factor,
+                             uint16_t* q_out, int64_t out_token_stride, int64_t out_head_stride, uint16_t* k_dq,
+                             uint16_t* v_dq, void* stream) {
+  const char* fn = "nvfp4_rope_append";
+  mxq::RopeArgs a = {};
+  mxq_status s = mxq::cache_args(fn, cache, block_table, ld_table, table_width, seq_lens, q_offsets, num_requests, tokens,
+                                 &a.p.c);
+  if (s != MXQ_OK) return s;
+  const int D = cache->head_dim;
+  if (num_q_heads < 1 || num_q_heads > 32767) return fail(MXQ_EINVAL, "%s: num_q_heads must be 1 to 32767", fn);
+  if (rotary_dim < 16 || rotary_dim > D || rotary_dim % 16)
+    return fail(MXQ_ESHAPE, "%s: rotary_dim must be a multiple of 16 up to head_dim (%d, %d)", fn, rotary_dim, D);
+  if (!isfinite(factor)) return fail(MXQ_EINVAL, "%s: factor is not finite", fn);
+  if (tokens == 0 || num_requests == 0) return ok();
+  if ((s = mxq::check_rows(fn, "q", q, q_token_stride, q_head_stride, D)) != MXQ_OK) return s;
+  if ((s = mxq::check_rows(fn, "q_out", q_out, out_token_stride, out_head_stride, D)) != MXQ_OK) return s;
+  if ((s = mxq::check_rows(fn, "k", k, k_token_stride, k_head_stride, D)) != MXQ_OK) return s;
+  if ((s = mxq::check_rows(fn, "v", v, v_token_stride, v_head_stride, D)) != MXQ_OK) return s;
+  if (!inv_freq) return fail(MXQ_EINVAL, "%s: inv_freq is NULL", fn);
+  if (!aligned(inv_freq, 4)) return fail(MXQ_EALIGN, "%s: inv_freq 4-byte aligned", fn);
+  if (!aligned16(k_dq) || !aligned16(v_dq)) return fail(MXQ_EALIGN, "%s: k_dq and v_dq 16-byte aligned", fn);
+  if (tokens >= (1 << 26)) return fail(MXQ_EUNSUPPORTED, "%s: too many rows for one call", fn);    // 32-bit grid
+  a.p.k = k;
+  a.p.v = v;
+  a.p.T = tokens;
+  a.p.k_token = k_token_stride;
+  a.p.k_head = k_head_stride;
+  a.p.v_token = v_token_stride;
+  a.p.v_head = v_head_stride;
+  a.p.k_dq = k_dq;
+  a.p.v_dq = v_dq;
+  a.q = q;
+  a.Hq = num_q_heads;
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
+  a.q_out = q_out;
+  a.o_token = out_token_stride;
+  a.o_head = out_head_stride;
+  a.inv_freq = inv_freq;
+  a.rot = rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.factor = factor;
+  return hip_status(mxq::launch_rope_append(a, S(stream)), fn);
+}
+
 }  // extern "C"

@@ -96,4 +96,18 @@ hipError_t launch_moe_dispatch(const MoeRowsArgs& a, hipStream_t st);
 hipError_t launch_moe_combine(const MoeRowsArgs& a, hipStream_t st);
 hipError_t launch_moe_combine_backward(const MoeRowsArgs& a, hipStream_t st);
 
+struct RopeArgs {
+  AppendArgs p;                 // k, v and the cache
+  const uint16_t* q;
+  int Hq;
+  int64_t q_token, q_head;      // strides, elements
+  uint16_t* q_out;
+  int64_t o_token, o_head;
+  const float* inv_freq;        // [rot / 2]
+  int rot, interleaved;
+  double factor;
+  int split;                    // waves of a token (set by the launcher)
+};
+hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st);
+
 }  // namespace mxq

@@ -1,6 +1,7 @@
 """Binding of the steps around a layer's products (include/mxq_layer.h): the
 root-mean-square norm with a quantized output, the router of a layer with
-experts, the rows of its tokens ordered by expert and back, each with its gradient.
+experts, the rows of its tokens ordered by expert and back, each with its
+gradient; rotary positions on the way into the NVFP4 cache.
 
 Like decode.py: argument marshalling and host checks only, outputs and
 workspaces the caller does not pass are allocated with torch, and every call is
@@ -13,11 +14,11 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import Format, Layout, lib
-from .decode import _check_tensor, _launch, _p, _takes_stream
+from .decode import _Cache, _check_requests, _check_rows, _check_tensor, _launch, _p, _takes_stream
 
 __all__ = ["RMSNorm", "mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace",
            "MoERows", "MoERouting", "mx_moe_route", "mx_moe_route_backward", "mx_moe_sort", "mx_moe_workspace",
-           "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward"]
+           "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward", "nvfp4_rope_append"]
 
 _fns = None
 
@@ -38,7 +39,9 @@ def _lib():
         L.mx_moe_dispatch.argtypes = [vp, i64, i64, i64, vp, i32, vp, i64, i64, vp]
         L.mx_moe_combine.argtypes = [vp, i64, i64, vp, vp, i64, i64, i32, vp, i64, vp]
         L.mx_moe_combine_backward.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, i64, i32, vp, i64, vp, vp]
-        for f in ("mx_rmsnorm", "mx_rmsnorm_backward", "mx_moe_route", "mx_moe_route_backward", "mx_moe_sort",
+        L.nvfp4_rope_append.argtypes = [vp, i64, i64, i32, vp, i64, i64, vp, i64, i64, i64, ctypes.POINTER(_Cache), vp, i64,
+                                        i64, vp, vp, i64, vp, i32, i32, ctypes.c_double, vp, i64, i64, vp, vp, vp]
+        for f in ("nvfp4_rope_append", "mx_rmsnorm", "mx_rmsnorm_backward", "mx_moe_route", "mx_moe_route_backward", "mx_moe_sort",
                   "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("mx_rmsnorm_backward_workspace", "mx_moe_workspace"):
@@ -339,3 +342,42 @@ def mx_moe_combine_backward(dout, rows, row_of, weights, drows=None, dweights=No
     _launch(dev, _lib().mx_moe_combine_backward, dout.data_ptr(), ld_d, rows.data_ptr(), ld_rows, M, row_of.data_ptr(),
             weights.data_ptr(), T, cols, k, drows.data_ptr(), ld_dr, dweights.data_ptr())
     return drows, dweights
+
+
+# ------------------------------------------------- positions, on the way to the cache
+
+@_takes_stream
+def nvfp4_rope_append(q, k, v, cache, block_table, seq_lens, inv_freq, q_offsets=None, interleaved=False, factor=1.0,
+                      out=None, with_dq=False, k_dq=None, v_dq=None):
+    """nvfp4_cache_append with rotary positions: the first 2 * len(inv_freq)
+    values of every head of the BF16 rows q [tokens, q_heads, head_dim] and k are
+    turned by position * inv_freq (float32; pairs are the two halves, or
+    neighbours with interleaved), cosine and sine times `factor`; then k and v
+    [tokens, heads, head_dim] are quantized into the cache.  Requests as in
+    nvfp4_cache_append.  Returns the turned q (out may be q itself), or
+    (q, k_dq, v_dq) with with_dq (or k_dq and v_dq); rows of no request are not written."""
+    T = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
+    dev, n, width, ld = _check_requests(cache, block_table, seq_lens, q_offsets, T)
+    h, d = cache.num_heads, cache.head_dim
+    hq, qt, qh = _check_rows(q, "q", None, d, T, dev)
+    _, kt, kh = _check_rows(k, "k", h, d, T, dev)
+    _, vt, vh = _check_rows(v, "v", h, d, T, dev)
+    _check_tensor(inv_freq, "inv_freq", torch.float32, 1, dev)
+    if not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous")
+    if out is None:
+        out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
+        ot, oh = hq * d, d
+    else:
+        _, ot, oh = _check_rows(out, "out", hq, d, T, dev)
+    if with_dq or k_dq is not None or v_dq is not None:
+        k_dq = torch.empty((T, h, d), dtype=torch.bfloat16, device=dev) if k_dq is None else k_dq
+        v_dq = torch.empty((T, h, d), dtype=torch.bfloat16, device=dev) if v_dq is None else v_dq
+        for name, t in (("k_dq", k_dq), ("v_dq", v_dq)):
+            _check_rows(t, name, h, d, T, dev)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    _launch(dev, _lib().nvfp4_rope_append, q.data_ptr(), qt, qh, hq, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, T,
+            cache._ref, block_table.data_ptr(), ld, width, seq_lens.data_ptr(), _p(q_offsets), n, inv_freq.data_ptr(),
+            2 * inv_freq.numel(), bool(interleaved), factor, out.data_ptr(), ot, oh, _p(k_dq), _p(v_dq))
+    return out if k_dq is None else (out, k_dq, v_dq)

@@ -126,3 +126,25 @@ def combine_ref(rows, row_of, weights):
     out = t.sum(1)
     e = (k + 1) * 2 * EPS_F32 * np.abs(t).sum(1)
     return out, EPS_BF16 * np.abs(out) + (1 + EPS_BF16) * e + TINY_BF16
+
+
+# ------------------------------------------------------------ rotary positions
+
+def turned_bits(bits, pos, inv_freq, interleaved, factor=1.0):
+    """Rows bits [n, heads, D] (BF16) at positions pos [n] turned by the steps of the definition: BF16 bits."""
+    x = f64(bits).astype(np.float32)
+    rot = 2 * len(inv_freq)
+    angle = np.asarray(pos, np.float64)[:, None] * np.asarray(inv_freq, np.float32).astype(np.float64)
+    c = (np.cos(angle) * factor).astype(np.float32)[:, None]
+    s = (np.sin(angle) * factor).astype(np.float32)[:, None]
+    a, b = (x[..., 0:rot:2], x[..., 1:rot:2]) if interleaved else (x[..., :rot // 2], x[..., rot // 2:rot])
+    with np.errstate(all="ignore"):
+        u, v = a * c - b * s, b * c + a * s
+    out = x.copy()
+    if interleaved:
+        out[..., 0:rot:2], out[..., 1:rot:2] = u, v
+    else:
+        out[..., :rot // 2], out[..., rot // 2:rot] = u, v
+    res = F.bf16_rne(out.astype(np.float64))
+    res[..., rot:] = bits[..., rot:]
+    return res

@@ -17,5 +17,6 @@ hipError_t launch_moe_route_backward(const RouteBwdArgs&, hipStream_t) { return 
 hipError_t launch_moe_dispatch(const MoeRowsArgs&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_moe_combine(const MoeRowsArgs&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_moe_combine_backward(const MoeRowsArgs&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_rope_append(const RopeArgs&, hipStream_t) { return hipErrorNoDevice; }
 
 }  // namespace mxq

@@ -19,7 +19,8 @@ FAKE = ctypes.c_void_p(0x10000)       # never dereferenced: validation fails fir
 ODD = ctypes.c_void_p(0x10008)
 EINVAL, ESHAPE, EALIGN, EUNSUPPORTED = 1, 2, 3, 4
 NAMES = ["mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace", "mx_moe_route", "mx_moe_route_backward",
-         "mx_moe_sort", "mx_moe_workspace", "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward"]
+         "mx_moe_sort", "mx_moe_workspace", "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward",
+         "nvfp4_rope_append"]
 
 
 def _lib():
@@ -196,6 +197,33 @@ def test_moe_binding_refuses_before_the_library_is_called():
                  lambda: m.mx_moe_route_backward(x, x, i, x), lambda: m.mx_moe_route(None, 2)):
         with pytest.raises(TypeError):
             call()                                             # not on a GPU
+
+
+def test_rope_append_rejects_bad_arguments():
+    m, L = _lib()
+    from microscaling_quantization_block_amd import decode as d
+    from tests.test_decode_abi import BAD_CACHE, _cache
+
+    def call(q=FAKE, qs=(1024, 128), hq=8, k=FAKE, ks=(256, 128), v=FAKE, vs=(256, 128), tokens=3, cache=(), table=FAKE, ld=4,
+             width=4, lens=FAKE, offs=None, n=3, freq=FAKE, rot=128, inter=0, factor=1.0, out=FAKE, os_=(1024, 128), kd=None,
+             vd=None):
+        c = ctypes.byref(_cache(d, **dict(cache)))
+        return L.nvfp4_rope_append(q, *qs, hq, k, *ks, v, *vs, tokens, c, table, ld, width, lens, offs, n, freq, rot, inter,
+                                   factor, out, *os_, kd, vd, None)
+
+    for kw, status in BAD_CACHE:
+        assert call(cache=kw.items()) == status, kw
+    for kw in (dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(freq=None), dict(lens=None), dict(table=None),
+               dict(tokens=-1), dict(n=-1), dict(width=-1), dict(ld=3), dict(tokens=4), dict(ks=(-8, 128)), dict(hq=0),
+               dict(hq=32768), dict(factor=float("nan")), dict(factor=float("inf"))):
+        assert call(**kw) == EINVAL, kw
+    for kw in (dict(rot=0), dict(rot=8), dict(rot=24), dict(rot=144), dict(rot=-16)):
+        assert call(**kw) == ESHAPE, kw
+    for kw in (dict(q=ODD), dict(k=ODD), dict(out=ODD), dict(vs=(256, 100)), dict(qs=(1020, 128)), dict(os_=(1024, 100)),
+               dict(kd=ODD), dict(vd=ODD), dict(freq=ctypes.c_void_p(0x10002))):
+        assert call(**kw) == EALIGN, kw
+    assert call(tokens=1 << 26, offs=FAKE) == EUNSUPPORTED and call(tokens=1 << 31, offs=FAKE) == EUNSUPPORTED
+    assert call(tokens=0, n=0) == 0 and call(tokens=0, offs=FAKE) == 0
 
 
 def _runtime(name):
