@@ -18,8 +18,6 @@
 #include "lanes.h"
 #include "layer_kernels.h"
 
-#include <type_traits>
-
 namespace mxq {
 
 namespace {
@@ -36,22 +34,32 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);      // 0xFFFFFFFF: a NaN
 }
 
-__device__ __forceinline__ float logit(const void* logits, int f32, int64_t i) {
-  if (f32) return static_cast<const float*>(logits)[i];
+template <bool F32>
+__device__ __forceinline__ float logit(const void* logits, int64_t i) {
+  if constexpr (F32) return static_cast<const float*>(logits)[i];
   return __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[i] << 16);
+}
+
+// The logits of this lane, all loads in flight at once: a lane beyond the last
+// expert reads that one (a load in a branch of its own would be waited for there).
+template <int LANES, int VPL, bool F32>
+__device__ __forceinline__ void load_logits(const void* logits, int64_t at, int E, int lane, float* x) {
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) x[v] = logit<F32>(logits, at + min(v * LANES + lane, E - 1));
 }
 
 constexpr int SORT_WAVES = 8;
 
 // Routes token t (LANES lanes, `lane` of them); counts its experts in hist.
-template <int LANES, int VPL>
+template <int LANES, int VPL, bool F32>
 __device__ __forceinline__ void route_token(const MoeArgs& a, int64_t t, int lane, int* hist) {
+  float x[VPL];
+  load_logits<LANES, VPL, F32>(a.logits, t * a.ld, a.E, lane, x);
   uint32_t key[VPL];
   uint32_t top = 0;
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
-    const int e = v * LANES + lane;
-    key[v] = e < a.E ? key_of(logit(a.logits, a.f32, t * a.ld + e)) : 0u;
+    key[v] = v * LANES + lane < a.E ? key_of(x[v]) : 0u;
     top = umax(top, key[v]);
   }
   top = lanes_max<LANES>(top);
@@ -59,8 +67,10 @@ __device__ __forceinline__ void route_token(const MoeArgs& a, int64_t t, int lan
   float all = 0.0f;
   if (!a.renorm) {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v)
-      if (key[v]) all += expf(value_of(key[v]) - largest);
+    for (int v = 0; v < VPL; ++v) {
+      const float p = expf(x[v] - largest);
+      all += v * LANES + lane < a.E ? p : 0.0f;
+    }
     all = lanes_sum<LANES>(all);
   }
   int mine = -1;                               // lane j: the expert of slot j and its key
@@ -224,24 +234,24 @@ __device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int6
     if (r >= rows) a.row_token[r] = 0;
 }
 
-template <int LANES, int VPL>
+template <int LANES, int VPL, bool F32>
 __global__ __launch_bounds__(256) void route_kernel(MoeArgs a) {
   extern __shared__ int lds[];
   for (int i = threadIdx.x; i < a.E; i += 256) lds[i] = 0;
   __syncthreads();
   const int64_t first = blockIdx.x * a.group_tokens, last = min(a.T, first + a.group_tokens);
   for (int64_t t = first + threadIdx.x / LANES; t < last; t += 256 / LANES)
-    route_token<LANES, VPL>(a, t, threadIdx.x & (LANES - 1), lds);
+    route_token<LANES, VPL, F32>(a, t, threadIdx.x & (LANES - 1), lds);
   __syncthreads();
   const int pad = (a.E + 7) / 8 * 8;
   for (int i = threadIdx.x; i < pad; i += 256) a.counts[blockIdx.x * (int64_t)pad + i] = (uint16_t)(i < a.E ? lds[i] : 0);
 }
 
-template <int LANES, int VPL>
+template <int LANES, int VPL, bool F32>
 __global__ __launch_bounds__(1024) void route_one_kernel(MoeArgs a) {
   extern __shared__ int lds[];
   for (int64_t t = threadIdx.x / LANES; t < a.T; t += 1024 / LANES)
-    route_token<LANES, VPL>(a, t, threadIdx.x & (LANES - 1), lds);     // its counts are not used
+    route_token<LANES, VPL, F32>(a, t, threadIdx.x & (LANES - 1), lds);     // its counts are not used
   __syncthreads();
   sort_slots<1024, false>(a, 0, 0, a.T * a.k, lds);
 }
@@ -273,7 +283,7 @@ __global__ __launch_bounds__(1024) void sort_one_kernel(MoeArgs a) {
 
 // dl of the softmax: over the chosen experts w_j (dw_j - sum w dw); over all of
 // them p_e (dw_e - sum w dw), dw_e 0 where e was not chosen.
-template <int LANES, int VPL>
+template <int LANES, int VPL, bool F32>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
   const int lane = threadIdx.x & (LANES - 1);
   const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
@@ -289,10 +299,10 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
     for (int v = 0; v < VPL; ++v) d[v] = 0.0f;
   } else {
     float x[VPL], top = -__builtin_inff(), total = 0.0f;
+    load_logits<LANES, VPL, F32>(a.logits, t * a.ld, a.E, lane, x);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const int e = v * LANES + lane;
-      x[v] = e < a.E ? logit(a.logits, a.f32, t * a.ld + e) : -__builtin_inff();
+      x[v] = v * LANES + lane < a.E ? x[v] : -__builtin_inff();
       top = fmaxf(top, x[v]);
     }
     top = value_of(lanes_max<LANES>(key_of(top)));
@@ -318,24 +328,34 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
   for (int v = 0; v < VPL; ++v) {
     const int e = v * LANES + lane;
     if (e >= a.E) continue;
-    if (a.f32) static_cast<float*>(a.dlogits)[t * a.ld_d + e] = d[v];
+    if constexpr (F32) static_cast<float*>(a.dlogits)[t * a.ld_d + e] = d[v];
     else static_cast<uint16_t*>(a.dlogits)[t * a.ld_d + e] = (uint16_t)f32x2_to_bf16x2(d[v], 0.0f);
   }
 }
 
-// Calls f<LANES, VPL>() for E experts and k choices: 16 lanes a token up to 256 experts (four tokens a wave: for 128
+template <int LANES_, int VPL_, bool F32_>
+struct Lanes {
+  static constexpr int LANES = LANES_, VPL = VPL_;
+  static constexpr bool F32 = F32_;
+};
+
+// Calls f with a Lanes for E experts and k choices: 16 lanes a token up to 256 experts (four tokens a wave: for 128
 // experts a round is 50 instructions for all four), a wave beyond, and where 16 lanes cannot hold the choices.
-template <class F>
+template <bool F32, class F>
 hipError_t with_lanes(int E, int k, F&& f) {
   if (k <= 16) {
-    if (E <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
-    if (E <= 64) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
-    if (E <= 128) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 8>());
-    if (E <= 256) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
+    if (E <= 16) return f(Lanes<16, 1, F32>());
+    if (E <= 64) return f(Lanes<16, 4, F32>());
+    if (E <= 128) return f(Lanes<16, 8, F32>());
+    if (E <= 256) return f(Lanes<16, 16, F32>());
   }
-  if (E <= 256) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
-  if (E <= 512) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
-  return f(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
+  if (E <= 256) return f(Lanes<64, 4, F32>());
+  if (E <= 512) return f(Lanes<64, 8, F32>());
+  return f(Lanes<64, 16, F32>());
+}
+template <class F>
+hipError_t with_lanes(bool f32, int E, int k, F&& f) {
+  return f32 ? with_lanes<true>(E, k, f) : with_lanes<false>(E, k, f);
 }
 
 }  // namespace
@@ -354,12 +374,12 @@ void plan_moe(MoeArgs& a, bool routed) {
 }
 
 hipError_t launch_moe_route(const MoeArgs& a, hipStream_t st) {
-  const hipError_t e = with_lanes(a.E, a.k, [&](auto lanes, auto vpl) {
-    constexpr int LANES = decltype(lanes)::value, VPL = decltype(vpl)::value;
+  const hipError_t e = with_lanes(a.f32, a.E, a.k, [&](auto lanes) {
+    using W = decltype(lanes);
     if (!a.groups)
-      hipLaunchKernelGGL((route_one_kernel<LANES, VPL>), dim3(1), dim3(1024), sort_lds(a.E), st, a);
+      hipLaunchKernelGGL((route_one_kernel<W::LANES, W::VPL, W::F32>), dim3(1), dim3(1024), sort_lds(a.E), st, a);
     else
-      hipLaunchKernelGGL((route_kernel<LANES, VPL>), dim3((unsigned)a.groups), dim3(256), (size_t)a.E * 4, st, a);
+      hipLaunchKernelGGL((route_kernel<W::LANES, W::VPL, W::F32>), dim3((unsigned)a.groups), dim3(256), (size_t)a.E * 4, st, a);
     return hipGetLastError();
   });
   if (e != hipSuccess || !a.groups) return e;
@@ -380,10 +400,10 @@ hipError_t launch_moe_sort(const MoeArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_moe_route_backward(const RouteBwdArgs& a, hipStream_t st) {
-  return with_lanes(a.E, a.k, [&](auto lanes, auto vpl) {
-    constexpr int LANES = decltype(lanes)::value, VPL = decltype(vpl)::value;
-    const int64_t grid = (a.T + 256 / LANES - 1) / (256 / LANES);
-    hipLaunchKernelGGL((route_backward_kernel<LANES, VPL>), dim3((unsigned)grid), dim3(256), 0, st, a);
+  return with_lanes(a.f32, a.E, a.k, [&](auto lanes) {
+    using W = decltype(lanes);
+    const int64_t tokens = 256 / W::LANES, grid = (a.T + tokens - 1) / tokens;
+    hipLaunchKernelGGL((route_backward_kernel<W::LANES, W::VPL, W::F32>), dim3((unsigned)grid), dim3(256), 0, st, a);
     return hipGetLastError();
   });
 }
@@ -396,62 +416,75 @@ __device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret
 __device__ __forceinline__ void store16(uint16_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
 
 // 2^lx lanes hold 8 2^lx columns of a token; 256 / 2^lx tokens a workgroup.
+// UNIFORM (lx >= 6): a wave holds one token, whose rows and weights are scalar loads.
 struct Place {
   int64_t t, c;                                // token, first column
   bool there;
 };
+template <bool UNIFORM>
 __device__ __forceinline__ Place place_of(const MoeRowsArgs& a, int lx) {
   Place p;
-  p.t = (int64_t)blockIdx.x * (256 >> lx) + (threadIdx.x >> lx);
+  const int own = threadIdx.x >> lx;
+  p.t = (int64_t)blockIdx.x * (256 >> lx) + (UNIFORM ? __builtin_amdgcn_readfirstlane(own) : own);
   p.c = (((int64_t)blockIdx.y << lx) + (threadIdx.x & ((1 << lx) - 1))) * 8;
   p.there = p.t < a.T && p.c < a.cols;
   return p;
 }
 
+// The rows of B slots from j0 on, -1 for none.  All of them are loaded before
+// one is used: a load behind the first row's would wait for that row.
+template <int B>
+__device__ __forceinline__ void rows_of(const MoeRowsArgs& a, const int32_t* row_of, int j0, int* r) {
+  const int rows = (int)a.M;
+#pragma unroll
+  for (int j = 0; j < B; ++j) r[j] = row_of[min(j0 + j, a.k - 1)];
+#pragma unroll
+  for (int j = 0; j < B; ++j) r[j] = r[j] < rows && j0 + j < a.k ? r[j] : -1;      // negative ones pass through
+}
+
+template <int B, bool UNIFORM>
 __global__ __launch_bounds__(256) void dispatch_kernel(MoeRowsArgs a, int lx) {
-  const Place p = place_of(a, lx);
+  const Place p = place_of<UNIFORM>(a, lx);
   if (!p.there) return;
   const uint4 v = load16(a.x + p.t * a.ld_x + p.c);
-  const int32_t* row_of = a.row_of + p.t * a.k;
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t r = row_of[j];
-    if (r >= 0 && r < a.M) store16(a.to_rows + r * a.ld_to + p.c, v);
+  for (int j0 = 0; j0 < a.k; j0 += B) {
+    int r[B];
+    rows_of<B>(a, a.row_of + p.t * a.k, j0, r);
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+      if (r[j] >= 0) store16(a.to_rows + r[j] * a.ld_to + p.c, v);
   }
 }
 
+template <int B, bool UNIFORM, bool WEIGHTS>
 __global__ __launch_bounds__(256) void combine_kernel(MoeRowsArgs a, int lx) {
-  const Place p = place_of(a, lx);
+  const Place p = place_of<UNIFORM>(a, lx);
   if (!p.there) return;
-  const int32_t* row_of = a.row_of + p.t * a.k;
-  const float* weights = a.weights ? a.weights + p.t * a.k : nullptr;
   float sum[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
-  constexpr int B = 8;                         // rows in flight
-  for (int j0 = 0; j0 < a.k; j0 += B) {
-    uint4 v[B];
+  for (int j0 = 0; j0 < a.k && a.M > 0; j0 += B) {
+    int r[B];
     float w[B];
-    bool has[B];
+    uint4 v[B];
+    rows_of<B>(a, a.row_of + p.t * a.k, j0, r);
+#pragma unroll
+    for (int j = 0; j < B; ++j) w[j] = WEIGHTS ? a.weights[p.t * a.k + min(j0 + j, a.k - 1)] : 1.0f;
+    // a slot without a row reads row 0, so that all B rows are in flight, and counts
+    // as zeros times zero, whatever that row and its weight hold
+#pragma unroll
+    for (int j = 0; j < B; ++j) v[j] = load16(a.rows + max(r[j], 0) * a.ld_rows + p.c);
 #pragma unroll
     for (int j = 0; j < B; ++j) {
-      has[j] = false;
-      if (j0 + j < a.k) {
-        const int64_t r = row_of[j0 + j];
-        has[j] = r >= 0 && r < a.M;
-        w[j] = weights ? weights[j0 + j] : 1.0f;
-        if (has[j]) v[j] = load16(a.rows + r * a.ld_rows + p.c);
+      const uint32_t keep = r[j] >= 0 ? 0xFFFFFFFFu : 0u;
+      const float f = __uint_as_float(__float_as_uint(w[j]) & keep);
+      const uint32_t u[4] = {v[j].x & keep, v[j].y & keep, v[j].z & keep, v[j].w & keep};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum[2 * i] = __builtin_fmaf(f, bf16_lo(u[i]), sum[2 * i]);
+        sum[2 * i + 1] = __builtin_fmaf(f, bf16_hi(u[i]), sum[2 * i + 1]);
       }
     }
-#pragma unroll
-    for (int j = 0; j < B; ++j)
-      if (has[j]) {
-        const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum[2 * i] = __builtin_fmaf(w[j], bf16_lo(u[i]), sum[2 * i]);
-          sum[2 * i + 1] = __builtin_fmaf(w[j], bf16_hi(u[i]), sum[2 * i + 1]);
-        }
-      }
   }
   store16(a.out + p.t * a.ld_out + p.c, make_uint4(f32x2_to_bf16x2(sum[0], sum[1]), f32x2_to_bf16x2(sum[2], sum[3]),
                                                    f32x2_to_bf16x2(sum[4], sum[5]), f32x2_to_bf16x2(sum[6], sum[7])));
@@ -460,9 +493,9 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeRowsArgs a, int lx) {
 // A wave per slot: drow = w dout, dw = dout . row.
 __global__ __launch_bounds__(256) void combine_backward_kernel(MoeRowsArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t s = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (s >= a.T * a.k) return;                  // whole waves leave
-  const int64_t t = s / a.k, r = a.row_of[s];
+  const uint32_t s = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (s >= (uint32_t)(a.T * a.k)) return;      // whole waves leave; slots stay below 2^27
+  const int64_t t = s / (uint32_t)a.k, r = a.row_of[s];
   if (r < 0 || r >= a.M) {                     // no row, no gradient
     if (lane == 0) a.dweights[s] = 0.0f;
     return;
@@ -470,22 +503,53 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(MoeRowsArgs a) {
   const float w = a.weights[s];
   const uint16_t *g = a.x + t * a.ld_x, *y = a.rows + r * a.ld_rows;
   uint16_t* d = a.to_rows + r * a.ld_to;
+  constexpr int B = 4;                         // chunks of a lane in flight
+  const int cols = (int)a.cols;
   float dot = 0.0f;
-#pragma unroll 4
-  for (int64_t c = 8 * lane; c < a.cols; c += 512) {
-    const uint4 gv = load16(g + c), yv = load16(y + c);
-    const uint32_t gu[4] = {gv.x, gv.y, gv.z, gv.w}, yu[4] = {yv.x, yv.y, yv.z, yv.w};
-    uint32_t o[4];
+  for (int c0 = 8 * lane; c0 < cols; c0 += 512 * B) {
+    uint4 gv[B], yv[B];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dot = __builtin_fmaf(bf16_lo(gu[i]), bf16_lo(yu[i]), dot);
-      dot = __builtin_fmaf(bf16_hi(gu[i]), bf16_hi(yu[i]), dot);
-      o[i] = f32x2_to_bf16x2(w * bf16_lo(gu[i]), w * bf16_hi(gu[i]));
+    for (int i = 0; i < B; ++i) {              // beyond the row: its last chunk, not used
+      const int c = min(c0 + 512 * i, cols - 8);
+      gv[i] = load16(g + c);
+      yv[i] = load16(y + c);
     }
-    store16(d + c, make_uint4(o[0], o[1], o[2], o[3]));
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (c0 + 512 * i >= cols) break;
+      const uint32_t gu[4] = {gv[i].x, gv[i].y, gv[i].z, gv[i].w}, yu[4] = {yv[i].x, yv[i].y, yv[i].z, yv[i].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        dot = __builtin_fmaf(bf16_lo(gu[j]), bf16_lo(yu[j]), dot);
+        dot = __builtin_fmaf(bf16_hi(gu[j]), bf16_hi(yu[j]), dot);
+        o[j] = f32x2_to_bf16x2(w * bf16_lo(gu[j]), w * bf16_hi(gu[j]));
+      }
+      store16(d + c0 + 512 * i, make_uint4(o[0], o[1], o[2], o[3]));
+    }
   }
   dot = lanes_sum<64>(dot);
   if (lane == 0) a.dweights[s] = dot;
+}
+
+template <int B_, bool UNIFORM_>
+struct Slots {
+  static constexpr int B = B_;
+  static constexpr bool UNIFORM = UNIFORM_;
+};
+
+// Calls f with a Slots: as many slots at once as a token has, up to eight.
+template <bool UNIFORM, class F>
+void with_slots(int k, F&& f) {
+  if (k <= 1) f(Slots<1, UNIFORM>());
+  else if (k <= 2) f(Slots<2, UNIFORM>());
+  else if (k <= 4) f(Slots<4, UNIFORM>());
+  else f(Slots<8, UNIFORM>());
+}
+template <class F>
+void with_slots(int k, int lx, F&& f) {
+  if (lx >= 6) with_slots<true>(k, f);
+  else with_slots<false>(k, f);
 }
 
 int lanes_log2(int64_t cols) {
@@ -502,13 +566,22 @@ dim3 rows_grid(const MoeRowsArgs& a, int lx) {
 
 hipError_t launch_moe_dispatch(const MoeRowsArgs& a, hipStream_t st) {
   const int lx = lanes_log2(a.cols);
-  hipLaunchKernelGGL(dispatch_kernel, rows_grid(a, lx), dim3(256), 0, st, a, lx);
+  const dim3 grid = rows_grid(a, lx);
+  with_slots(a.k, lx, [&](auto w) {
+    using W = decltype(w);
+    hipLaunchKernelGGL((dispatch_kernel<W::B, W::UNIFORM>), grid, dim3(256), 0, st, a, lx);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine(const MoeRowsArgs& a, hipStream_t st) {
   const int lx = lanes_log2(a.cols);
-  hipLaunchKernelGGL(combine_kernel, rows_grid(a, lx), dim3(256), 0, st, a, lx);
+  const dim3 grid = rows_grid(a, lx);
+  with_slots(a.k, lx, [&](auto w) {
+    using W = decltype(w);
+    if (a.weights) hipLaunchKernelGGL((combine_kernel<W::B, W::UNIFORM, true>), grid, dim3(256), 0, st, a, lx);
+    else hipLaunchKernelGGL((combine_kernel<W::B, W::UNIFORM, false>), grid, dim3(256), 0, st, a, lx);
+  });
   return hipGetLastError();
 }
 
