@@ -412,9 +412,6 @@ hipError_t launch_moe_route_backward(const RouteBwdArgs& a, hipStream_t st) {
 
 namespace {
 
-__device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ void store16(uint16_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
-
 // 2^lx lanes hold 8 2^lx columns of a token; 256 / 2^lx tokens a workgroup.
 // UNIFORM (lx >= 6): a wave holds one token, whose rows and weights are scalar loads.
 struct Place {
@@ -452,7 +449,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(MoeRowsArgs a, int lx) {
     rows_of<B>(a, a.row_of + p.t * a.k, j0, r);
 #pragma unroll
     for (int j = 0; j < B; ++j)
-      if (r[j] >= 0) store16(a.to_rows + r[j] * a.ld_to + p.c, v);
+      if (r[j] >= 0) store16_once(a.to_rows + r[j] * a.ld_to + p.c, v);
   }
 }
 
@@ -473,7 +470,7 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeRowsArgs a, int lx) {
     // a slot without a row reads row 0, so that all B rows are in flight, and counts
     // as zeros times zero, whatever that row and its weight hold
 #pragma unroll
-    for (int j = 0; j < B; ++j) v[j] = load16(a.rows + max(r[j], 0) * a.ld_rows + p.c);
+    for (int j = 0; j < B; ++j) v[j] = load16_once(a.rows + max(r[j], 0) * a.ld_rows + p.c);
 #pragma unroll
     for (int j = 0; j < B; ++j) {
       const uint32_t keep = r[j] >= 0 ? 0xFFFFFFFFu : 0u;
@@ -512,7 +509,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(MoeRowsArgs a) {
     for (int i = 0; i < B; ++i) {              // beyond the row: its last chunk, not used
       const int c = min(c0 + 512 * i, cols - 8);
       gv[i] = load16(g + c);
-      yv[i] = load16(y + c);
+      yv[i] = load16_once(y + c);
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {
@@ -525,7 +522,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(MoeRowsArgs a) {
         dot = __builtin_fmaf(bf16_hi(gu[j]), bf16_hi(yu[j]), dot);
         o[j] = f32x2_to_bf16x2(w * bf16_lo(gu[j]), w * bf16_hi(gu[j]));
       }
-      store16(d + c0 + 512 * i, make_uint4(o[0], o[1], o[2], o[3]));
+      store16_once(d + c0 + 512 * i, make_uint4(o[0], o[1], o[2], o[3]));
     }
   }
   dot = lanes_sum<64>(dot);

@@ -166,6 +166,20 @@ __device__ __forceinline__ u32x4 philox_draws8(uint64_t n, uint64_t seed, uint32
                        (uint32_t)seed, (uint32_t)(seed >> 32));
 }
 
+// ------------------------------------------------------------------ memory
+// 16 bytes; the second pair for data that this kernel touches once and that does
+// not stay in a cache until it is read again.
+__device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void store16(uint16_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
+typedef uint32_t mxq_u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 load16_once(const uint16_t* p) {
+  const mxq_u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const mxq_u32x4*>(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ void store16_once(uint16_t* p, uint4 v) {
+  __builtin_nontemporal_store(mxq_u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<mxq_u32x4*>(p));
+}
+
 // ------------------------------------------------------------------ lanes
 __device__ __forceinline__ uint32_t lane_xor_u32(uint32_t v, int mask) {
   return (uint32_t)__shfl_xor((int)v, mask, 64);

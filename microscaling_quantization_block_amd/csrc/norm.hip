@@ -74,9 +74,6 @@ __device__ __forceinline__ uint4 fp8_values8(uint2 codes, uint32_t s) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-__device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ void store16(uint16_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
-
 // LANES lanes (16 or 64) times WAVES waves hold a row, CH chunks a lane: chunk
 // lane + LANES (wave CH + i).  16 lanes hold a short row of one chunk a lane, four rows a wave.
 template <int LANES, int WAVES, int CH, int FMT>
@@ -136,7 +133,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
     if (a.h) {
 #pragma unroll
       for (int i = 0; i < CH; ++i)
-        if (c[i] < chunks) store16(a.h + row * a.ld_h + 8 * c[i], h[i]);
+        if (c[i] < chunks) store16_once(a.h + row * a.ld_h + 8 * c[i], h[i]);
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) h[i] = scaled8(h[i], rstd, w[i]);        // y from here on
@@ -160,7 +157,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
         if (c[i] < chunks) {
           *reinterpret_cast<uint2*>(a.codes + row * a.ld_codes + 8 * c[i]) = code;
           if (c[i] % LPB == 0) blk_store<F32S>(a.scales, scale_offset(row, c[i] / LPB, chunks / LPB, a.mfma), sc);
-          if (a.dq) store16(a.dq + row * a.ld_dq + 8 * c[i], fp8_values8<F32S>(code, sc));
+          if (a.dq) store16_once(a.dq + row * a.ld_dq + 8 * c[i], fp8_values8<F32S>(code, sc));
         }
       }
     }
@@ -190,7 +187,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
         if (c[i] < chunks) {
           *reinterpret_cast<uint32_t*>(a.codes + row * a.ld_codes + 4 * c[i]) = code;
           if ((c[i] & 1) == 0) a.scales[scale_offset(row, c[i] >> 1, chunks >> 1, a.mfma)] = (uint8_t)bs.code;
-          if (a.dq) store16(a.dq + row * a.ld_dq + 8 * c[i], nv_decode8(code, e4m3_to_f32(bs.code), S));
+          if (a.dq) store16_once(a.dq + row * a.ld_dq + 8 * c[i], nv_decode8(code, e4m3_to_f32(bs.code), S));
         }
       }
     }
@@ -244,16 +241,20 @@ hipError_t launch_rmsnorm(const NormArgs& a, mxq_format fmt, hipStream_t st) {
 //
 //   g = dy w,  xhat = h rstd,  dx = rstd (g - xhat mean(g xhat)) + dres,  dw = sum over rows of dy xhat
 //
-// The row sum and dw are binary32.  A workgroup walks rows and keeps dw of its
-// columns in registers; its sums go to the workspace, and a second kernel adds
-// them, always in the same order (no atomics).
+// The row sum and dw are binary32.  TEAMS teams of WAVES waves hold a row each;
+// a workgroup walks rows and keeps dw of its columns in registers; the teams'
+// sums meet in LDS, the workgroup's go to the workspace, and a second kernel adds those,
+// always in the same order (no atomics).
 
 namespace {
 
-template <int WAVES, int CH>
-__global__ __launch_bounds__(64 * WAVES) void rmsnorm_backward_kernel(NormBwdArgs a) {
-  __shared__ float part[2][WAVES];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <int WAVES, int TEAMS, int CH>
+__global__ __launch_bounds__(64 * WAVES * TEAMS) void rmsnorm_backward_kernel(NormBwdArgs a) {
+  constexpr int COLS = 512 * WAVES * CH;
+  __shared__ float part[2][TEAMS][WAVES];
+  __shared__ float team_dw[TEAMS > 1 ? COLS : 1];
+  const int lane = threadIdx.x & 63;
+  const int wave = (threadIdx.x >> 6) % WAVES, team = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) / WAVES);
   const int chunks = (int)(a.cols >> 3);
   const float inv = 1.0f / (float)a.cols;
   int c[CH];
@@ -267,16 +268,20 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_backward_kernel(NormBwdArg
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+  // every team takes every step, so that all waves meet at the barriers
+  for (int64_t row0 = (int64_t)blockIdx.x * TEAMS; row0 < a.rows; row0 += (int64_t)gridDim.x * TEAMS, turn ^= 1) {
+    const int64_t row = row0 + team;
+    const bool live = TEAMS == 1 || row < a.rows;
     uint4 dy[CH], h[CH], r[CH];
     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      dy[i] = c[i] < chunks ? load16(a.dy + row * a.ld_dy + 8 * c[i]) : zero;
-      h[i] = c[i] < chunks ? load16(a.h + row * a.ld_h + 8 * c[i]) : zero;
-      r[i] = a.dres && c[i] < chunks ? load16(a.dres + row * a.ld_dres + 8 * c[i]) : zero;
+      const bool has = live && c[i] < chunks;
+      dy[i] = has ? load16(a.dy + row * a.ld_dy + 8 * c[i]) : zero;
+      h[i] = has ? load16_once(a.h + row * a.ld_h + 8 * c[i]) : zero;
+      r[i] = a.dres && has ? load16(a.dres + row * a.ld_dres + 8 * c[i]) : zero;
     }
-    const float rstd = a.rstd[row];
+    const float rstd = live ? a.rstd[row] : 0.0f;
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -293,11 +298,11 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_backward_kernel(NormBwdArg
     }
     s = lanes_sum<64>(s);
     if constexpr (WAVES > 1) {
-      if (lane == 0) part[turn][wave] = s;
+      if (lane == 0) part[turn][team][wave] = s;
       __syncthreads();
       s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < WAVES; ++i) s += part[turn][i];
+      for (int i = 0; i < WAVES; ++i) s += part[turn][team][i];
     }
     const float m = s * inv;                                   // mean of g xhat
 #pragma unroll
@@ -311,64 +316,105 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_backward_kernel(NormBwdArg
         const float t1 = __builtin_fmaf(-(bf16_hi(x[j]) * rstd), m, bf16_hi(y[j]) * bf16_hi(g[j]));
         o[j] = f32x2_to_bf16x2(__builtin_fmaf(rstd, t0, bf16_lo(d[j])), __builtin_fmaf(rstd, t1, bf16_hi(d[j])));
       }
-      if (c[i] < chunks) store16(a.dx + row * a.ld_dx + 8 * c[i], make_uint4(o[0], o[1], o[2], o[3]));
+      if (live && c[i] < chunks) store16_once(a.dx + row * a.ld_dx + 8 * c[i], make_uint4(o[0], o[1], o[2], o[3]));
     }
   }
-  if (a.dw) {
-    float* p = a.part + (int64_t)blockIdx.x * a.cols;
+  if (!a.dw) return;                           // the same for all
+  if constexpr (TEAMS > 1) {
+    // the teams in turn, the last one keeps the sum
+    for (int k = 0; k < TEAMS; ++k) {
+      if (team == k) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
-      if (c[i] < chunks) {
-        float4* q = reinterpret_cast<float4*>(p + 8 * c[i]);
-        q[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-        q[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+        for (int i = 0; i < CH; ++i) {
+          float4* p = reinterpret_cast<float4*>(team_dw + 8 * c[i]);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float4 t = k ? p[q] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            t = make_float4(t.x + dw[i][4 * q], t.y + dw[i][4 * q + 1], t.z + dw[i][4 * q + 2], t.w + dw[i][4 * q + 3]);
+            dw[i][4 * q] = t.x;
+            dw[i][4 * q + 1] = t.y;
+            dw[i][4 * q + 2] = t.z;
+            dw[i][4 * q + 3] = t.w;
+            if (k < TEAMS - 1) p[q] = t;
+          }
+        }
       }
+      __syncthreads();
+    }
+    if (team != TEAMS - 1) return;
   }
+  float* p = a.part + (int64_t)blockIdx.x * a.cols;
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+    if (c[i] < chunks) {
+      float4* q = reinterpret_cast<float4*>(p + 8 * c[i]);
+      q[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+      q[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    }
 }
 
-// dw[c] = sum of the groups' part[g][c]: 32 columns a workgroup, 32 lanes of
-// groups, each in turn, then in the order of the lanes.
+// dw[c] = sum of the groups' part[g][c]: 32 columns a workgroup, eight lanes of
+// four each; 128 lanes of groups, each its groups in turn, then in the order of the lanes.
 __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* part, int64_t groups, int64_t cols, float* dw) {
-  __shared__ float s[32][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + x;
-  float sum = 0.0f;
+  __shared__ float4 s[128][9];
+  const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+  const int64_t c = ((int64_t)blockIdx.x * 8 + x) * 4;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (c < cols) {
 #pragma unroll 4
-    for (int64_t g = y; g < groups; g += 32) sum += part[g * cols + c];
+    for (int64_t g = y; g < groups; g += 128) {
+      const float4 v = *reinterpret_cast<const float4*>(part + g * cols + c);
+      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+    }
   }
   s[y][x] = sum;
   __syncthreads();
-  if (y == 0 && c < cols) {
-    float t = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) t += s[i][x];
-    dw[c] = t;
+  for (int n = 64; n >= 1; n /= 2) {
+    if (y < n) {
+      const float4 v = s[y + n][x];
+      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+      s[y][x] = sum;
+    }
+    __syncthreads();
   }
+  if (y == 0 && c < cols) *reinterpret_cast<float4*>(dw + c) = sum;
 }
 
-template <int WAVES, int CH>
+// The kernel's shape for a number of columns, and the workgroups that it runs on.
+struct BwdShape {
+  int teams;
+  int64_t most;
+};
+BwdShape bwd_shape(int64_t cols) {
+  if (cols <= 512) return {4, 1024};
+  if (cols <= 2048) return {4, 512};
+  if (cols <= 4096) return {2, 512};
+  return {1, cols <= 16384 ? 512 : 256};
+}
+
+template <int WAVES, int TEAMS, int CH>
 void launch_bwd(const NormBwdArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)norm_bwd_groups(a.rows, a.cols)), block(64 * WAVES);
-  hipLaunchKernelGGL((rmsnorm_backward_kernel<WAVES, CH>), grid, block, 0, st, a);
+  const dim3 grid((unsigned)norm_bwd_groups(a.rows, a.cols)), block(64 * WAVES * TEAMS);
+  hipLaunchKernelGGL((rmsnorm_backward_kernel<WAVES, TEAMS, CH>), grid, block, 0, st, a);
 }
 
 }  // namespace
 
 int64_t norm_bwd_groups(int64_t rows, int64_t cols) {
-  const int64_t most = cols <= 4096 ? 1024 : cols <= 16384 ? 512 : 256;
-  return rows < most ? rows : most;
+  const BwdShape s = bwd_shape(cols);
+  const int64_t need = (rows + s.teams - 1) / s.teams;
+  return need < s.most ? need : s.most;
 }
 
 hipError_t launch_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st) {
   const int64_t n = a.cols;
   if (a.rows == 0) {}                          // no rows: a sum of nothing
-  else if (n <= 512) launch_bwd<1, 1>(a, st);
-  else if (n <= 2048) launch_bwd<4, 1>(a, st);
-  else if (n <= 4096) launch_bwd<4, 2>(a, st);
-  else if (n <= 8192) launch_bwd<4, 4>(a, st);
-  else if (n <= 16384) launch_bwd<8, 4>(a, st);
-  else launch_bwd<16, 4>(a, st);
+  else if (n <= 512) launch_bwd<1, 4, 1>(a, st);
+  else if (n <= 2048) launch_bwd<1, 4, 4>(a, st);
+  else if (n <= 4096) launch_bwd<4, 2, 2>(a, st);
+  else if (n <= 8192) launch_bwd<4, 1, 4>(a, st);
+  else if (n <= 16384) launch_bwd<8, 1, 4>(a, st);
+  else launch_bwd<16, 1, 4>(a, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.dw) return e;
   hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((unsigned)((n + 31) / 32)), dim3(1024), 0, st, a.part,
