@@ -3,8 +3,8 @@
 //
 // Router: a token's k largest logits, ties to the lower expert, and their softmax weights
 // (over the chosen ones, or over all experts).  A token is 16 lanes or a wave, expert
-// v LANES + lane in lane; a round finds the largest key by lane exchanges, then the lowest
-// expert that has it, and takes it out.
+// v LANES + lane in lane.  Bound by its instructions and their latency: every
+// lane sorts its few logits once, and a round compares the lanes' first ones.
 //
 // Order: rows by (expert, token, slot), a counting sort.  Each group of tokens
 // counts its slots by expert; a second kernel adds the counts of the groups before its own
@@ -22,16 +22,64 @@ namespace mxq {
 
 namespace {
 
-// Binary32 values as unsigned integers of the same order.  Both zeros give one
-// key, a NaN the largest; 0 stands for an expert that is not there (any more).
-constexpr uint32_t KEY_MINUS_INF = 0x007FFFFFu;
-__device__ __forceinline__ uint32_t key_of(float x) {
+// A logit and its expert as one unsigned integer: larger logits are larger, and
+// of equal ones that of the lower expert.  The upper half orders values: both
+// zeros give one number, a NaN the largest.  0 stands for an expert that is not
+// there (any more).  Binary32 logits take 64 bits, BF16 ones 32.
+__device__ __forceinline__ uint32_t order_of(float x) {
   if (x != x) return 0xFFFFFFFFu;
   const uint32_t b = __float_as_uint(x + 0.0f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float value_of(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);      // 0xFFFFFFFF: a NaN
+__device__ __forceinline__ float value_of(uint32_t order) {
+  return __uint_as_float(order & 0x80000000u ? order & 0x7FFFFFFFu : ~order);      // 0xFFFFFFFF: a NaN
+}
+constexpr uint32_t ORDER_MINUS_INF = 0x007FFFFFu;
+
+template <bool F32>
+struct Key;
+template <>
+struct Key<true> {
+  using T = uint64_t;
+  static __device__ __forceinline__ T make(float x, int e) { return (uint64_t)order_of(x) << 32 | (uint32_t)~e; }
+  static __device__ __forceinline__ bool chosen(T k) { return (uint32_t)(k >> 32) > ORDER_MINUS_INF; }
+  static __device__ __forceinline__ float value(T k) { return value_of((uint32_t)(k >> 32)); }
+  static __device__ __forceinline__ int expert(T k) { return (int)~(uint32_t)k; }
+  template <int LANES>
+  static __device__ __forceinline__ T largest(T k) {
+    const uint32_t hi = lanes_max<LANES>((uint32_t)(k >> 32));
+    const uint32_t lo = lanes_max<LANES>((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+    return (uint64_t)hi << 32 | lo;
+  }
+};
+template <>
+struct Key<false> {
+  using T = uint32_t;
+  static __device__ __forceinline__ T make(float x, int e) { return (order_of(x) & 0xFFFF0000u) | (0xFFFFu - e); }
+  static __device__ __forceinline__ bool chosen(T k) { return k >> 16 > ORDER_MINUS_INF >> 16; }
+  static __device__ __forceinline__ float value(T k) { return value_of(k & 0x80000000u ? k & 0xFFFF0000u : k | 0xFFFFu); }
+  static __device__ __forceinline__ int expert(T k) { return 0xFFFF - (int)(k & 0xFFFFu); }
+  template <int LANES>
+  static __device__ __forceinline__ T largest(T k) { return lanes_max<LANES>(k); }
+};
+
+// Sorts a[0 .. N - 1], the largest first: Batcher's odd-even merge sort, all
+// places known at compile time.
+template <int N, class T>
+__device__ __forceinline__ void sort_down(T* a) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const T x = a[i + j], y = a[i + j + k];
+            a[i + j] = x > y ? x : y;
+            a[i + j + k] = x > y ? y : x;
+          }
 }
 
 template <bool F32>
@@ -50,20 +98,24 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t at, int 
 
 constexpr int SORT_WAVES = 8;
 
-// Routes token t (LANES lanes, `lane` of them); counts its experts in hist.
-template <int LANES, int VPL, bool F32>
-__device__ __forceinline__ void route_token(const MoeArgs& a, int64_t t, int lane, int* hist) {
+// Routes token t (LANES lanes, `lane` of them); `count` gets every slot and its expert
+// (-1: none).  A lane sorts its own keys once; a round then compares the lanes'
+// first ones and the lane that has the largest drops it.
+template <int LANES, int VPL, bool F32, class F>
+__device__ __forceinline__ void route_token(const MoeArgs& a, int64_t t, int lane, F&& count) {
+  using K = Key<F32>;
   float x[VPL];
   load_logits<LANES, VPL, F32>(a.logits, t * a.ld, a.E, lane, x);
-  uint32_t key[VPL];
-  uint32_t top = 0;
+  typename K::T key[VPL];
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
-    key[v] = v * LANES + lane < a.E ? key_of(x[v]) : 0u;
-    top = umax(top, key[v]);
+    const int e = v * LANES + lane;
+    const typename K::T k = K::make(x[v], e);
+    key[v] = e < a.E ? k : 0;
   }
-  top = lanes_max<LANES>(top);
-  const float largest = value_of(top);
+  sort_down<VPL>(key);
+  typename K::T top = K::template largest<LANES>(key[0]);
+  const float largest = K::value(top);
   float all = 0.0f;
   if (!a.renorm) {
 #pragma unroll
@@ -73,131 +125,156 @@ __device__ __forceinline__ void route_token(const MoeArgs& a, int64_t t, int lan
     }
     all = lanes_sum<LANES>(all);
   }
-  int mine = -1;                               // lane j: the expert of slot j and its key
-  uint32_t mine_key = 0;
+  typename K::T mine = 0;                      // lane j: the key of slot j
   for (int j = 0; j < a.k; ++j) {
-    if (j) {
-      top = 0;
+    if (!K::chosen(top)) break;                // nothing is left for this token
+    mine = lane == j ? top : mine;
+    // bit masks: of a choice between key[v] and key[v + 1] the compiler makes a
+    // choice of places, with a chain of comparisons for each
+    const typename K::T drop = key[0] == top ? ~(typename K::T)0 : 0;
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) top = umax(top, key[v]);
-      top = lanes_max<LANES>(top);
-    }
-    if (top <= KEY_MINUS_INF) break;           // nothing is left for this token
-    uint32_t low = 0;                          // ~expert: the largest is the lowest expert
-#pragma unroll
-    for (int v = VPL - 1; v >= 0; --v) low = key[v] == top ? ~(uint32_t)(v * LANES + lane) : low;
-    const int e = (int)~lanes_max<LANES>(low);
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) key[v] = v * LANES + lane == e ? 0u : key[v];
-    if (lane == j) {
-      mine = e;
-      mine_key = top;
-    }
+    for (int v = 0; v + 1 < VPL; ++v) key[v] = (key[v + 1] & drop) | (key[v] & ~drop);
+    key[VPL - 1] &= ~drop;
+    top = K::template largest<LANES>(key[0]);
   }
-  const float part = mine >= 0 ? expf(value_of(mine_key) - largest) : 0.0f;
+  const bool has = mine != 0;
+  const int e = has ? K::expert(mine) : -1;
+  const float part = has ? expf(K::value(mine) - largest) : 0.0f;
   const float total = a.renorm ? lanes_sum<LANES>(part) : all;
   if (lane < a.k) {
-    a.experts[t * a.k + lane] = mine;
-    a.weights[t * a.k + lane] = mine >= 0 ? part / total : 0.0f;
-    if (mine >= 0) atomicAdd(&hist[mine], 1);
+    a.experts[t * a.k + lane] = e;
+    a.weights[t * a.k + lane] = has ? part / total : 0.0f;
+    count(t * a.k + lane, e);
   }
 }
 
-// The number that goes before n counts of the workgroup's threads in turn: an
-// exclusive sum over threads.  `scratch` holds an int per wave.
+// Inclusive sum over the lanes of a wave: shifts inside 16 lanes, then the last
+// lanes of 16 and of 32 to those behind them.
+__device__ __forceinline__ int wave_running_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+}
+
+// The sum of n over the workgroup's threads before this one.  `scratch` holds an int per wave.
 template <int THREADS>
 __device__ __forceinline__ int block_exclusive_sum(int n, int* scratch) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int s = n;
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const int up = __shfl_up(s, o, 64);
-    if (lane >= o) s += up;
-  }
+  const int s = wave_running_sum(n);
   if (lane == 63) scratch[wave] = s;
   __syncthreads();
   int before = 0;
-  for (int i = 0; i < wave; ++i) before += scratch[i];
+#pragma unroll
+  for (int i = 0; i < THREADS / 64; ++i) before += i < wave ? scratch[i] : 0;
   return before + s - n;
 }
 
-// LDS of the sort: hist [SORT_WAVES, E], then total and before [E] each.
-inline size_t sort_lds(int E) { return (size_t)(SORT_WAVES + 2) * E * 4; }
+// LDS of the sort: two counts of every expert (of all groups, and of those before
+// this workgroup's) as one 64-bit number, then hist [SORT_WAVES, E].
+inline size_t sort_lds(int E) { return (size_t)E * 8 + (size_t)SORT_WAVES * E * 4; }
 
-// Gives the slots [first, last) of the call (this workgroup's) their rows.
+__device__ __forceinline__ int pieces_of_wave(int slots) { return ((slots + 63) / 64 + SORT_WAVES - 1) / SORT_WAVES; }
+__device__ __forceinline__ int* sort_hist(int* lds, int E) { return lds + 2 * E; }
+
+// Gives the slots [first, last) of the call (this workgroup's) their rows; `ids`
+// holds their experts, ids[0] that of slot `first`.
 // GROUPS: their counts and those of the other groups are in a.counts; else they are all there is.
-template <int THREADS, bool GROUPS>
-__device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int64_t first, int64_t last, int* lds) {
+// COUNTED: they are counted in hist, slot s in wave s / (64 pieces_of_wave).
+template <int THREADS, bool GROUPS, bool COUNTED>
+__device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int64_t first, int64_t last, const int* ids,
+                                           int* lds) {
   __shared__ int scratch[THREADS / 64];
   __shared__ int all_rows;
-  const int E = a.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int* hist = lds;
-  int* total = lds + SORT_WAVES * E;
-  int* before = total + E;
-  for (int i = threadIdx.x; i < (SORT_WAVES + 2) * E; i += THREADS) lds[i] = 0;
-  __syncthreads();
-  // whole 64-slot pieces of the workgroup's slots, in order, to the waves in order
-  const int64_t pieces = (last - first + 63) / 64, each = (pieces + SORT_WAVES - 1) / SORT_WAVES;
-  const int64_t from = first + wave * each * 64, to = min(last, from + each * 64);
-  if (wave < SORT_WAVES)
-    for (int64_t s = from + lane; s < to; s += 64) {
-      const int e = a.experts[s];
-      if ((unsigned)e < (unsigned)E) atomicAdd(&hist[wave * E + e], 1);
-    }
+  const int E = a.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, slots = (int)(last - first);
+  uint64_t* both = reinterpret_cast<uint64_t*>(lds);           // of all groups << 32 | of the groups before
+  int* hist = sort_hist(lds, E);
+
+  // a lane adds eight experts' counts over every (THREADS / lanes of a row)-th
+  // group; the first eight of them are on their way while the workgroup's own
+  // slots are counted
+  const int per_row = (E + 7) / 8, slices = THREADS / per_row;
+  const int col = threadIdx.x % per_row, slice = threadIdx.x / per_row;
+  constexpr int AHEAD = 8;
+  uint4 ahead[AHEAD];
   if constexpr (GROUPS) {
-    // a lane adds eight experts' counts over every (THREADS / lanes of a row)-th group
-    const int per_row = (E + 7) / 8, slices = THREADS / per_row;
-    const int c = threadIdx.x % per_row, slice = threadIdx.x / per_row;
-    int sum[8], pre[8];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int64_t g = min(slice + (int64_t)i * slices, a.groups - 1);
+      ahead[i] = *reinterpret_cast<const uint4*>(a.counts + (g * per_row + col) * 8);
+    }
+  }
+  if constexpr (!COUNTED)
+    for (int i = threadIdx.x; i < (SORT_WAVES + 2) * E; i += THREADS) lds[i] = 0;
+  // whole 64-slot pieces of the workgroup's slots, in order, to the waves in order
+  const int each = pieces_of_wave(slots), from = wave * each * 64;
+  const int to = min(slots, from + each * 64);
+  const auto expert_at = [&](int s) {          // E stands for no expert
+    const int e = s < to ? ids[s] : -1;
+    return (unsigned)e < (unsigned)E ? e : E;
+  };
+  const int first_e = wave < SORT_WAVES ? expert_at(from + lane) : E;
+  if constexpr (!COUNTED) {
+    __syncthreads();
+    if (wave < SORT_WAVES)
+      for (int s0 = from; s0 < to; s0 += 64) {
+        const int e = s0 == from ? first_e : expert_at(s0 + lane);
+        if (e < E) atomicAdd(&hist[wave * E + e], 1);
+      }
+  }
+  if constexpr (GROUPS) {
+    uint32_t sum[8], pre[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] = pre[i] = 0;
-    if (slice < slices) {
-#pragma unroll 4
-      for (int64_t g = slice; g < a.groups; g += slices) {
-        const uint4 w = *reinterpret_cast<const uint4*>(a.counts + (g * per_row + c) * 8);
-        const uint32_t n[4] = {w.x, w.y, w.z, w.w};
+    const auto add = [&](uint4 w, int64_t g) {
+      const uint32_t n[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t in = g < a.groups ? 0xFFFFFFFFu : 0u, earlier = g < group ? 0xFFFFFFFFu : 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int lo = (int)(n[i] & 0xFFFFu), hi = (int)(n[i] >> 16);
-          sum[2 * i] += lo;
-          sum[2 * i + 1] += hi;
-          pre[2 * i] += g < group ? lo : 0;
-          pre[2 * i + 1] += g < group ? hi : 0;
-        }
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = n[i] & 0xFFFFu, hi = n[i] >> 16;
+        sum[2 * i] += lo & in;
+        sum[2 * i + 1] += hi & in;
+        pre[2 * i] += lo & earlier;
+        pre[2 * i + 1] += hi & earlier;
       }
+    };
+    if (slice < slices) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) add(ahead[i], slice + (int64_t)i * slices);
+#pragma unroll 4
+      for (int64_t g = slice + (int64_t)AHEAD * slices; g < a.groups; g += slices)
+        add(*reinterpret_cast<const uint4*>(a.counts + (g * per_row + col) * 8), g);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c * 8 + i < E) {
-          atomicAdd(&total[c * 8 + i], sum[i]);
-          atomicAdd(&before[c * 8 + i], pre[i]);
-        }
+        if (col * 8 + i < E)
+          atomicAdd(reinterpret_cast<unsigned long long*>(&both[col * 8 + i]), (unsigned long long)sum[i] << 32 | pre[i]);
     }
-    __syncthreads();
-  } else {
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += THREADS) {
-      int n = 0;
-#pragma unroll
-      for (int w = 0; w < SORT_WAVES; ++w) n += hist[w * E + e];
-      total[e] = n;
-    }
-    __syncthreads();
   }
+  if constexpr (!COUNTED) __syncthreads();
   // the experts' first rows, then those of this workgroup's waves
+  const auto total = [&](int e) {
+    if constexpr (GROUPS) return (int)(both[e] >> 32);
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < SORT_WAVES; ++w) n += hist[w * E + e];
+    return n;
+  };
   const int per = (E + THREADS - 1) / THREADS, e0 = min(E, (int)threadIdx.x * per), e1 = min(E, e0 + per);
   int n = 0;
-  for (int e = e0; e < e1; ++e) n += total[e];
+  for (int e = e0; e < e1; ++e) n += total(e);
   int start = block_exclusive_sum<THREADS>(n, scratch);
   for (int e = e0; e < e1; ++e) {
     if (group == 0) a.offsets[e] = start;
-    int at = start + before[e];
+    int at = start + (GROUPS ? (int)(uint32_t)both[e] : 0);
+    start += total(e);
 #pragma unroll
     for (int w = 0; w < SORT_WAVES; ++w) {
       const int m = hist[w * E + e];
       hist[w * E + e] = at;
       at += m;
     }
-    start += total[e];
   }
   if (threadIdx.x == THREADS - 1) {            // the last thread's end is the sum of all
     if (group == 0) a.offsets[E] = start;
@@ -205,12 +282,11 @@ __device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int6
   }
   __syncthreads();
   const int64_t rows = all_rows;
-  const int bits = 32 - __clz(E);              // of numbers up to E, which stands for no expert
+  const int bits = 32 - __clz(E);              // of numbers up to E
   if (wave < SORT_WAVES)
-    for (int64_t s0 = from; s0 < to; s0 += 64) {
-      const int64_t s = s0 + lane;
-      int e = s < to ? a.experts[s] : E;
-      e = (unsigned)e < (unsigned)E ? e : E;
+    for (int s0 = from; s0 < to; s0 += 64) {
+      const int s = s0 + lane;
+      const int e = s0 == from ? first_e : expert_at(s);
       uint64_t same = ~0ull;                   // lanes with this expert
       for (int b = 0; b < bits; ++b) {
         const bool one = (e >> b) & 1;
@@ -225,8 +301,9 @@ __device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int6
       // the next piece's counts come after this one's
       __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
       if (s < to) {
-        a.row_of[s] = e < E ? at : -1;
-        if (e < E) a.row_token[at] = (int)(s / a.k);
+        const int64_t slot = first + s;
+        a.row_of[slot] = e < E ? at : -1;
+        if (e < E) a.row_token[at] = (int)((uint32_t)slot / (uint32_t)a.k);      // slots stay below 2^27
       }
     }
   // rows of no slot: token 0, a row that a gather may read
@@ -234,30 +311,46 @@ __device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int6
     if (r >= rows) a.row_token[r] = 0;
 }
 
+constexpr int ROUTE_THREADS = 512;
+
 template <int LANES, int VPL, bool F32>
-__global__ __launch_bounds__(256) void route_kernel(MoeArgs a) {
-  extern __shared__ int lds[];
-  for (int i = threadIdx.x; i < a.E; i += 256) lds[i] = 0;
+__global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a) {
+  extern __shared__ __align__(16) int lds[];
+  for (int i = threadIdx.x; i < a.E; i += ROUTE_THREADS) lds[i] = 0;
   __syncthreads();
   const int64_t first = blockIdx.x * a.group_tokens, last = min(a.T, first + a.group_tokens);
-  for (int64_t t = first + threadIdx.x / LANES; t < last; t += 256 / LANES)
-    route_token<LANES, VPL, F32>(a, t, threadIdx.x & (LANES - 1), lds);
+  for (int64_t t = first + threadIdx.x / LANES; t < last; t += ROUTE_THREADS / LANES)
+    route_token<LANES, VPL, F32>(a, t, threadIdx.x & (LANES - 1), [&](int64_t, int e) {
+      if (e >= 0) atomicAdd(&lds[e], 1);
+    });
   __syncthreads();
   const int pad = (a.E + 7) / 8 * 8;
-  for (int i = threadIdx.x; i < pad; i += 256) a.counts[blockIdx.x * (int64_t)pad + i] = (uint16_t)(i < a.E ? lds[i] : 0);
+  for (int i = threadIdx.x; i < pad; i += ROUTE_THREADS)
+    a.counts[blockIdx.x * (int64_t)pad + i] = (uint16_t)(i < a.E ? lds[i] : 0);
 }
+
+// Tokens that one workgroup routes and sorts: their experts stay in LDS.
+constexpr int ONE_TOKENS = 64;
 
 template <int LANES, int VPL, bool F32>
 __global__ __launch_bounds__(1024) void route_one_kernel(MoeArgs a) {
-  extern __shared__ int lds[];
-  for (int64_t t = threadIdx.x / LANES; t < a.T; t += 1024 / LANES)
-    route_token<LANES, VPL, F32>(a, t, threadIdx.x & (LANES - 1), lds);     // its counts are not used
+  extern __shared__ __align__(16) int lds[];
+  __shared__ int ids[ONE_TOKENS * LANES];      // topk is at most LANES
+  int* hist = sort_hist(lds, a.E);
+  for (int i = threadIdx.x; i < SORT_WAVES * a.E; i += 1024) hist[i] = 0;
   __syncthreads();
-  sort_slots<1024, false>(a, 0, 0, a.T * a.k, lds);
+  const int of_wave = 64 * pieces_of_wave((int)a.T * a.k);
+  for (int64_t t = threadIdx.x / LANES; t < a.T; t += 1024 / LANES)
+    route_token<LANES, VPL, F32>(a, t, threadIdx.x & (LANES - 1), [&](int64_t slot, int e) {
+      ids[slot] = e;
+      if (e >= 0) atomicAdd(&hist[(int)slot / of_wave * a.E + e], 1);
+    });
+  __syncthreads();
+  sort_slots<1024, false, true>(a, 0, 0, a.T * a.k, ids, lds);
 }
 
 __global__ __launch_bounds__(256) void count_kernel(MoeArgs a) {
-  extern __shared__ int lds[];
+  extern __shared__ __align__(16) int lds[];
   for (int i = threadIdx.x; i < a.E; i += 256) lds[i] = 0;
   __syncthreads();
   const int64_t first = blockIdx.x * a.group_tokens * a.k, last = min(a.T * a.k, first + a.group_tokens * a.k);
@@ -271,14 +364,14 @@ __global__ __launch_bounds__(256) void count_kernel(MoeArgs a) {
 }
 
 __global__ __launch_bounds__(512) void sort_kernel(MoeArgs a) {
-  extern __shared__ int lds[];
+  extern __shared__ __align__(16) int lds[];
   const int64_t slots = a.T * a.k, each = a.group_tokens * a.k, first = blockIdx.x * each;
-  sort_slots<512, true>(a, blockIdx.x, first, min(slots, first + each), lds);
+  sort_slots<512, true, false>(a, blockIdx.x, first, min(slots, first + each), a.experts + first, lds);
 }
 
 __global__ __launch_bounds__(1024) void sort_one_kernel(MoeArgs a) {
-  extern __shared__ int lds[];
-  sort_slots<1024, false>(a, 0, 0, a.T * a.k, lds);
+  extern __shared__ __align__(16) int lds[];
+  sort_slots<1024, false, false>(a, 0, 0, a.T * a.k, a.experts, lds);
 }
 
 // dl of the softmax: over the chosen experts w_j (dw_j - sum w dw); over all of
@@ -288,11 +381,12 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
   const int lane = threadIdx.x & (LANES - 1);
   const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   if (t >= a.T) return;                        // whole groups of LANES lanes leave
-  const int32_t* ids = a.experts + t * a.k;
-  const float *w = a.weights + t * a.k, *dw = a.dweights + t * a.k;
-  float mean = 0.0f;
-  for (int j = 0; j < a.k; ++j)
-    if (ids[j] >= 0) mean = __builtin_fmaf(w[j], dw[j], mean);
+  // lane j holds slot j (topk is at most LANES)
+  const int64_t slot = t * a.k + min(lane, a.k - 1);
+  const int id = a.experts[slot];
+  const float w = a.weights[slot], dw = a.dweights[slot];
+  const bool has = lane < a.k && id >= 0;
+  const float mean = lanes_sum<LANES>(has ? w * dw : 0.0f);
   float d[VPL];
   if (a.renorm) {
 #pragma unroll
@@ -305,7 +399,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
       x[v] = v * LANES + lane < a.E ? x[v] : -__builtin_inff();
       top = fmaxf(top, x[v]);
     }
-    top = value_of(lanes_max<LANES>(key_of(top)));
+    top = value_of(lanes_max<LANES>(order_of(top)));
     // a token whose experts are all masked has weights of zero: nothing flows
     const float base = top > -__builtin_inff() ? top : 0.0f;
 #pragma unroll
@@ -318,9 +412,10 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
 #pragma unroll
     for (int v = 0; v < VPL; ++v) d[v] = -(x[v] * r) * mean;
   }
+  const float own = has ? w * (a.renorm ? dw - mean : dw) : 0.0f;
   for (int j = 0; j < a.k; ++j) {
-    const int e = ids[j];
-    const float g = w[j] * (a.renorm ? dw[j] - mean : dw[j]);
+    const int e = __shfl(id, j, LANES);
+    const float g = __shfl(own, j, LANES);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) d[v] += e == v * LANES + lane ? g : 0.0f;
   }
@@ -364,8 +459,8 @@ void plan_moe(MoeArgs& a, bool routed) {
   a.groups = 0;
   a.group_tokens = a.T;
   // one workgroup routes 64 tokens in a pass, or sorts a few thousand slots
-  if (routed ? a.T <= 64 : a.T * a.k <= 4096) return;
-  // 32 tokens a workgroup of the router are two passes; up to 256 groups beyond that, while counts fit 16 bits
+  if (routed ? a.T <= ONE_TOKENS : a.T * a.k <= 4096) return;
+  // 32 tokens are one pass of a workgroup of the router; up to 256 groups beyond that, while counts fit 16 bits
   int64_t each = (a.T + 255) / 256;
   each = each < 32 ? 32 : each;
   const int64_t most = 65535 / a.k;
@@ -379,7 +474,8 @@ hipError_t launch_moe_route(const MoeArgs& a, hipStream_t st) {
     if (!a.groups)
       hipLaunchKernelGGL((route_one_kernel<W::LANES, W::VPL, W::F32>), dim3(1), dim3(1024), sort_lds(a.E), st, a);
     else
-      hipLaunchKernelGGL((route_kernel<W::LANES, W::VPL, W::F32>), dim3((unsigned)a.groups), dim3(256), (size_t)a.E * 4, st, a);
+      hipLaunchKernelGGL((route_kernel<W::LANES, W::VPL, W::F32>), dim3((unsigned)a.groups), dim3(ROUTE_THREADS), (size_t)a.E * 4,
+                         st, a);
     return hipGetLastError();
   });
   if (e != hipSuccess || !a.groups) return e;

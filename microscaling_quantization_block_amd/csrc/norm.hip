@@ -225,15 +225,15 @@ hipError_t launch_rmsnorm(const NormArgs& a, mxq_format fmt, hipStream_t st) {
   const int64_t n = a.cols;
   if (n <= 128) return launch_norm<16, 1, 1>(a, fmt, st);
   if (n <= 512) return launch_norm<64, 1, 1>(a, fmt, st);
-  // a wave a row where that makes a wave for every SIMD, else four
-  if (a.rows >= 1024) {
-    if (n <= 1024) return launch_norm<64, 1, 2>(a, fmt, st);
+  if (n <= 1024) return launch_norm<64, 1, 2>(a, fmt, st);
+  // a wave a row where that makes two for every SIMD, else four and more
+  if (a.rows >= 2048) {
     if (n <= 2048) return launch_norm<64, 1, 4>(a, fmt, st);
     if (n <= 4096) return launch_norm<64, 1, 8>(a, fmt, st);
   }
   if (n <= 4096) return launch_norm<64, 4, 2>(a, fmt, st);
-  if (n <= 8192) return launch_norm<64, 4, 4>(a, fmt, st);
-  if (n <= 16384) return launch_norm<64, 4, 8>(a, fmt, st);
+  if (n <= 8192) return launch_norm<64, 8, 2>(a, fmt, st);
+  if (n <= 16384) return launch_norm<64, 16, 2>(a, fmt, st);
   return launch_norm<64, 16, 4>(a, fmt, st);
 }
 
@@ -248,9 +248,17 @@ hipError_t launch_rmsnorm(const NormArgs& a, mxq_format fmt, hipStream_t st) {
 
 namespace {
 
+// Keeps the compiler from holding what it computed of v before (binary32 values
+// take twice the registers of v itself).
+__device__ __forceinline__ void opaque(uint4& v) { asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
+
 template <int WAVES, int TEAMS, int CH>
 __global__ __launch_bounds__(64 * WAVES * TEAMS) void rmsnorm_backward_kernel(NormBwdArgs a) {
   constexpr int COLS = 512 * WAVES * CH;
+  // the widest rows: 16 waves have 128 registers a lane, so the weight is read
+  // where it is used, dres behind the row's sum, and nothing that was computed of
+  // dy and h before is kept (4096 rows of 32768: 626 us with all of it in registers, 311 so)
+  constexpr bool LEAN = COLS > 16384;
   __shared__ float part[2][TEAMS][WAVES];
   __shared__ float team_dw[TEAMS > 1 ? COLS : 1];
   const int lane = threadIdx.x & 63;
@@ -263,7 +271,7 @@ __global__ __launch_bounds__(64 * WAVES * TEAMS) void rmsnorm_backward_kernel(No
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     c[i] = lane + 64 * (wave * CH + i);
-    w[i] = c[i] < chunks ? load16(a.w + 8 * c[i]) : make_uint4(0, 0, 0, 0);
+    if (!LEAN) w[i] = c[i] < chunks ? load16(a.w + 8 * c[i]) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
@@ -279,7 +287,8 @@ __global__ __launch_bounds__(64 * WAVES * TEAMS) void rmsnorm_backward_kernel(No
       const bool has = live && c[i] < chunks;
       dy[i] = has ? load16(a.dy + row * a.ld_dy + 8 * c[i]) : zero;
       h[i] = has ? load16_once(a.h + row * a.ld_h + 8 * c[i]) : zero;
-      r[i] = a.dres && has ? load16(a.dres + row * a.ld_dres + 8 * c[i]) : zero;
+      if (!LEAN) r[i] = a.dres && has ? load16(a.dres + row * a.ld_dres + 8 * c[i]) : zero;
+      if (LEAN) w[i] = has ? load16(a.w + 8 * c[i]) : zero;
     }
     const float rstd = live ? a.rstd[row] : 0.0f;
     float s = 0.0f;
@@ -307,6 +316,15 @@ __global__ __launch_bounds__(64 * WAVES * TEAMS) void rmsnorm_backward_kernel(No
     const float m = s * inv;                                   // mean of g xhat
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
+      if (LEAN) {
+        opaque(dy[i]);
+        opaque(h[i]);
+      }
+      if (LEAN) {
+        const bool has = live && c[i] < chunks;
+        w[i] = has ? load16(a.w + 8 * c[i]) : zero;
+        r[i] = a.dres && has ? load16(a.dres + row * a.ld_dres + 8 * c[i]) : zero;
+      }
       const uint32_t y[4] = {dy[i].x, dy[i].y, dy[i].z, dy[i].w}, x[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
       const uint32_t g[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, d[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
       uint32_t o[4];
@@ -410,10 +428,10 @@ hipError_t launch_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st) {
   const int64_t n = a.cols;
   if (a.rows == 0) {}                          // no rows: a sum of nothing
   else if (n <= 512) launch_bwd<1, 4, 1>(a, st);
-  else if (n <= 2048) launch_bwd<1, 4, 4>(a, st);
+  else if (n <= 2048) launch_bwd<2, 4, 2>(a, st);
   else if (n <= 4096) launch_bwd<4, 2, 2>(a, st);
-  else if (n <= 8192) launch_bwd<4, 1, 4>(a, st);
-  else if (n <= 16384) launch_bwd<8, 1, 4>(a, st);
+  else if (n <= 8192) launch_bwd<8, 1, 2>(a, st);
+  else if (n <= 16384) launch_bwd<16, 1, 2>(a, st);
   else launch_bwd<16, 1, 4>(a, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.dw) return e;
