@@ -63,27 +63,53 @@ __global__ __launch_bounds__(256) void rope_append_kernel(RopeArgs a) {
   constexpr int PAIRS = INTERLEAVED ? 4 : 8;   // of a lane
   __shared__ float2 turns[4][D / 2];
   const CacheArgs& c = a.p.c;
-  const int wave = threadIdx.x >> 6, in_wave = threadIdx.x & 63, lane = in_wave & (L - 1);
-  const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
-  const int64_t t = unit / a.split;
+  // the wave's number in a scalar register, so that what it looks up by its token
+  // are scalar loads, which wait for no vector load
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), in_wave = threadIdx.x & 63, lane = in_wave & (L - 1);
+  const uint32_t unit = blockIdx.x * 4 + wave, token = unit / (uint32_t)a.split;
+  const int64_t t = token;
   if (t >= a.p.T) return;                      // whole waves
+  constexpr int ANGLES = (D / 2 + 63) / 64;    // of a lane
+  float freq[ANGLES];
+#pragma unroll
+  for (int i = 0; i < ANGLES; ++i) freq[i] = a.inv_freq[min(in_wave + 64 * i, a.rot / 2 - 1)];
+
+  // the token's heads: q, k, v in turn; this wave's share of them
+  const int heads = a.Hq + 2 * c.H, passes = (heads + ROWS - 1) / ROWS;
+  const int share = (int)(unit - token * (uint32_t)a.split);
+  const int first = passes * share / a.split, last = passes * (share + 1) / a.split;
+  const int own = in_wave / L;
+  // where the token's k and v lie from its q, and the strides of the heads, as plain
+  // numbers in scalar registers: a choice between kernel arguments would be loaded, row by row
+  const uint16_t* q = a.q + t * a.q_token;
+  int64_t to_k = (a.p.k + t * a.p.k_token) - q, to_v = (a.p.v + t * a.p.v_token) - q;
+  int64_t q_head = a.q_head, k_head = a.p.k_head, v_head = a.p.v_head;
+  asm("" : "+s"(to_k), "+s"(to_v), "+s"(q_head), "+s"(k_head), "+s"(v_head));
+  const auto load = [&](int p0, uint4* x) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int h = (p0 + i) * ROWS + own, kv = h - a.Hq;
+      const bool is_q = kv < 0, is_k = kv < c.H;
+      const uint16_t* head = q + (is_q ? h * q_head : is_k ? to_k + kv * k_head : to_v + (kv - c.H) * v_head);
+      x[i] = p0 + i < last && h < heads ? load16_once(head + 8 * lane) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  // on their way while the request, the page and the angles are found
+  uint4 x[BATCH];
+  load(first, x);
+
   RequestRows rows;
   const int64_t b = request_of(c, t, a.p.T, rows);
   if (b < 0) return;
   const int64_t pos = (int64_t)c.seq_lens[b] - rows.len + (t - rows.begin);
   const int64_t page = page_of(c, b, pos);
 
-  // the token's heads: q, k, v in turn; this wave's share of them
-  const int heads = a.Hq + 2 * c.H, passes = (heads + ROWS - 1) / ROWS;
-  const int share = (int)(unit - t * a.split);
-  const int first = passes * share / a.split, last = passes * (share + 1) / a.split;
-  const int own = in_wave / L;
-
   float2* turn = turns[wave];
-  for (int i = in_wave; i < a.rot / 2; i += 64) {
+#pragma unroll
+  for (int i = 0; i < ANGLES; ++i) {
     double co, si;
-    cos_sin((double)pos * (double)a.inv_freq[i], co, si);
-    turn[i] = make_float2((float)(co * a.factor), (float)(si * a.factor));
+    cos_sin((double)pos * (double)freq[i], co, si);
+    if (in_wave + 64 * i < a.rot / 2) turn[in_wave + 64 * i] = make_float2((float)(co * a.factor), (float)(si * a.factor));
   }
   // the wave's own writes, before any of its lanes reads them
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -105,15 +131,7 @@ __global__ __launch_bounds__(256) void rope_append_kernel(RopeArgs a) {
   const int partner = in_wave - lane + (second ? lane - half : lane + half);
 
   for (int p0 = first; p0 < last; p0 += BATCH) {
-    uint4 x[BATCH];
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int h = (p0 + i) * ROWS + own;
-      const uint16_t* src = h < a.Hq ? a.q + t * a.q_token + h * a.q_head
-                            : h < a.Hq + c.H ? a.p.k + t * a.p.k_token + (h - a.Hq) * a.p.k_head
-                                             : a.p.v + t * a.p.v_token + (h - a.Hq - c.H) * a.p.v_head;
-      x[i] = p0 + i < last && h < heads ? *reinterpret_cast<const uint4*>(src + 8 * lane) : make_uint4(0, 0, 0, 0);
-    }
+    if (p0 > first) load(p0, x);
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       const int h = (p0 + i) * ROWS + own;
@@ -139,7 +157,7 @@ __global__ __launch_bounds__(256) void rope_append_kernel(RopeArgs a) {
       const bool is_v = h >= a.Hq + c.H;
       const uint4 y = turned && !is_v ? make_uint4(o[0], o[1], o[2], o[3]) : x[i];
       if (h < a.Hq) {
-        *reinterpret_cast<uint4*>(a.q_out + t * a.o_token + h * a.o_head + 8 * lane) = y;
+        store16_once(a.q_out + t * a.o_token + h * a.o_head + 8 * lane, y);
       } else {
         const int kv = is_v ? h - a.Hq - c.H : h - a.Hq;
         uint16_t* dq = is_v ? a.p.v_dq : a.p.k_dq;
