@@ -50,28 +50,42 @@ def _lib():
     return _fns
 
 
+# These calls are short: a check that passes costs one function call, and an output like an input is
+# torch.empty_like of it (half the time of torch.empty).
+
 def _matrix(t, name, rows, cols, dev, dtype=torch.bfloat16):
     """A [rows, cols] matrix with unit column stride; returns its row stride (that of a single row means nothing)."""
-    _check_tensor(t, name, dtype, 2, dev)
-    if tuple(t.shape) != (rows, cols):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == (rows, cols)):
+        _check_tensor(t, name, dtype, 2, dev)
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return t.stride(0) if rows > 1 else cols
+    return ld if rows > 1 else cols
 
 
 def _flat(t, name, dtype, n, dev):
+    """A contiguous tensor of n entries."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.numel() == n and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.device != dev or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name} must be contiguous on {dev} with {n} entries")
+    raise ValueError(f"{name} must be contiguous on {dev} with {n} entries")
+
+
+def _workspace(need, workspace, like):
+    """A workspace and its size: the caller's, or a new one where `need` bytes are."""
+    if workspace is None:
+        return (like.new_empty(need, dtype=torch.uint8), need) if need else (None, 0)
+    _check_tensor(workspace, "workspace", torch.uint8, 1, like.device)
+    return workspace, workspace.numel() if workspace.is_contiguous() else 0
 
 
 def _first(x, name):
     """Rows, columns and device of the matrix that a call goes by."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda:
         raise TypeError(f"{name} must be a 2-D CUDA tensor")
-    return x.shape[0], x.shape[1], x.device
+    return *x.shape, x.device
 
 
 # --------------------------------------------------------------------- the norm
@@ -102,45 +116,47 @@ def mx_rmsnorm(x, weight, eps=1e-6, residual=None, fmt=Format.BF16, layout=Layou
     adds the codes' values in BF16, with_rstd what mx_rmsnorm_backward takes.
     Returns an RMSNorm.  h may be x or residual itself."""
     rows, cols, dev = _first(x, "x")
-    fmt = Format(fmt)
+    if type(fmt) is not Format:
+        fmt = Format(fmt)
     ld_x = _matrix(x, "x", rows, cols, dev)
     _flat(weight, "weight", torch.bfloat16, cols, dev)
-    bf16 = lambda: torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    ld_r = ld_h = ld_y = ld_c = ld_dq = 0
+    ld_r = ld_h = ld_y = ld_c = ld_dq = cols
     if residual is not None:
         ld_r = _matrix(residual, "residual", rows, cols, dev)
-        h = bf16() if h is None else h
-        ld_h = _matrix(h, "h", rows, cols, dev)
+        if h is None:
+            h = torch.empty_like(x)
+        else:
+            ld_h = _matrix(h, "h", rows, cols, dev)
     elif h is not None:
         raise ValueError("h without a residual is x")
-    if y is None and (with_y or fmt == Format.BF16):
-        y = bf16()
     if y is not None:
         ld_y = _matrix(y, "y", rows, cols, dev)
-    if rstd is None and with_rstd:
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    elif rstd is not None:
+    elif with_y or fmt is Format.BF16:
+        y = torch.empty_like(x)
+    if rstd is not None:
         _flat(rstd, "rstd", torch.float32, rows, dev)
-    if fmt == Format.BF16:
+    elif with_rstd:
+        rstd = x.new_empty(rows, dtype=torch.float32)
+    if fmt is Format.BF16:
         if with_dq or any(t is not None for t in (codes, scales, gscales, dq)):
             raise ValueError("BF16 output has no codes")
     else:
-        width = cols // 2 if fmt == Format.NVFP4 else cols
-        sdt = torch.float32 if fmt == Format.FP8_B128_F32 else torch.uint8
+        width = cols // 2 if fmt is Format.NVFP4 else cols
+        sdt = torch.float32 if fmt is Format.FP8_B128_F32 else torch.uint8
         blocks = cols // _BLOCK[fmt]
-        codes = torch.empty((rows, width), dtype=torch.uint8, device=dev) if codes is None else codes
+        codes = x.new_empty((rows, width), dtype=torch.uint8) if codes is None else codes
         ld_c = _matrix(codes, "codes", rows, width, dev, torch.uint8)
-        scales = torch.empty((rows, blocks), dtype=sdt, device=dev) if scales is None else scales
+        scales = x.new_empty((rows, blocks), dtype=sdt) if scales is None else scales
         _flat(scales, "scales", sdt, rows * blocks, dev)
-        if fmt == Format.NVFP4:
-            gscales = torch.empty(rows, dtype=torch.float32, device=dev) if gscales is None else gscales
+        if fmt is Format.NVFP4:
+            gscales = x.new_empty(rows, dtype=torch.float32) if gscales is None else gscales
             _flat(gscales, "gscales", torch.float32, rows, dev)
         elif gscales is not None:
             raise ValueError("gscales are NVFP4's")
-        if dq is None and with_dq:
-            dq = bf16()
         if dq is not None:
             ld_dq = _matrix(dq, "dq", rows, cols, dev)
+        elif with_dq:
+            dq = torch.empty_like(x)
     _launch(dev, _lib().mx_rmsnorm, x.data_ptr(), ld_x, _p(residual), ld_r, weight.data_ptr(), rows, cols, eps, _p(h), ld_h,
             _p(y), ld_y, _p(rstd), int(fmt), int(layout), _p(codes), ld_c, _p(scales), _p(gscales), _p(dq), ld_dq)
     return RMSNorm(y, h, rstd, codes, scales, gscales, dq)
@@ -163,19 +179,17 @@ def mx_rmsnorm_backward(dy, h, weight, rstd, dresidual=None, dx=None, dweight=No
     _flat(weight, "weight", torch.bfloat16, cols, dev)
     _flat(rstd, "rstd", torch.float32, rows, dev)
     ld_dr = 0 if dresidual is None else _matrix(dresidual, "dresidual", rows, cols, dev)
-    dx = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if dx is None else dx
-    ld_dx = _matrix(dx, "dx", rows, cols, dev)
-    have = 0
-    if dweight is None and with_dweight:
-        dweight = torch.empty(cols, dtype=torch.float32, device=dev)
+    ld_dx, have = cols, 0
+    if dx is None:
+        dx = torch.empty_like(dy)
+    else:
+        ld_dx = _matrix(dx, "dx", rows, cols, dev)
     if dweight is not None:
         _flat(dweight, "dweight", torch.float32, cols, dev)
-        if workspace is None:
-            have = _lib().mx_rmsnorm_backward_workspace(rows, cols)
-            workspace = torch.empty(have, dtype=torch.uint8, device=dev)
-        else:
-            _check_tensor(workspace, "workspace", torch.uint8, 1, dev)
-            have = workspace.numel() if workspace.is_contiguous() else 0
+    elif with_dweight:
+        dweight = dy.new_empty(cols, dtype=torch.float32)
+    if dweight is not None:
+        workspace, have = _workspace(_lib().mx_rmsnorm_backward_workspace(rows, cols), workspace, dy)
     _launch(dev, _lib().mx_rmsnorm_backward, dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, weight.data_ptr(), rstd.data_ptr(),
             _p(dresidual), ld_dr, rows, cols, dx.data_ptr(), ld_dx, _p(dweight), _p(workspace), have)
     return dx, dweight
@@ -200,21 +214,18 @@ class MoERouting(NamedTuple):
     row_of: torch.Tensor
 
 
-def _rows_out(T, E, k, dev, offsets, row_token, row_of):
-    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device=dev)
-    offsets = i32(E + 1) if offsets is None else offsets
-    row_token = i32(T * k) if row_token is None else row_token
-    row_of = i32(T, k) if row_of is None else row_of
-    for t, name, n in ((offsets, "offsets", E + 1), (row_token, "row_token", T * k), (row_of, "row_of", T * k)):
-        _flat(t, name, torch.int32, n, dev)
-    return offsets, row_token, row_of
+def _given(t, name, shape, dtype, like):
+    """An output: the caller's, of that many entries, or a new one on `like`'s device."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    _flat(t, name, dtype, shape if isinstance(shape, int) else shape[0] * shape[1], like.device)
+    return t
 
 
-def _workspace(need, workspace, dev):
-    if workspace is None:
-        return (torch.empty(need, dtype=torch.uint8, device=dev), need) if need else (None, 0)
-    _check_tensor(workspace, "workspace", torch.uint8, 1, dev)
-    return workspace, workspace.numel() if workspace.is_contiguous() else 0
+def _rows_out(T, E, k, like, offsets, row_token, row_of):
+    i32 = torch.int32
+    return (_given(offsets, "offsets", E + 1, i32, like), _given(row_token, "row_token", T * k, i32, like),
+            _given(row_of, "row_of", (T, k), i32, like))
 
 
 def _logits(t, name, T, E, dev):
@@ -239,12 +250,10 @@ def mx_moe_route(logits, topk, renormalize=True, experts=None, weights=None, off
     a_row_index or x_row_index, row_of and weights to mx_moe_combine."""
     T, E, dev = _first(logits, "logits")
     ld = _logits(logits, "logits", T, E, dev)
-    experts = torch.empty((T, topk), dtype=torch.int32, device=dev) if experts is None else experts
-    weights = torch.empty((T, topk), dtype=torch.float32, device=dev) if weights is None else weights
-    _flat(experts, "experts", torch.int32, T * topk, dev)
-    _flat(weights, "weights", torch.float32, T * topk, dev)
-    offsets, row_token, row_of = _rows_out(T, E, topk, dev, offsets, row_token, row_of)
-    workspace, have = _workspace(_lib().mx_moe_workspace(T, E, topk), workspace, dev)
+    experts = _given(experts, "experts", (T, topk), torch.int32, logits)
+    weights = _given(weights, "weights", (T, topk), torch.float32, logits)
+    offsets, row_token, row_of = _rows_out(T, E, topk, logits, offsets, row_token, row_of)
+    workspace, have = _workspace(_lib().mx_moe_workspace(T, E, topk), workspace, logits)
     _launch(dev, _lib().mx_moe_route, logits.data_ptr(), logits.dtype is torch.float32, ld, T, E, topk, bool(renormalize),
             experts.data_ptr(), weights.data_ptr(), offsets.data_ptr(), row_token.data_ptr(), row_of.data_ptr(),
             _p(workspace), have)
@@ -263,8 +272,10 @@ def mx_moe_route_backward(dweights, logits, experts, weights, renormalize=True, 
     _flat(experts, "experts", torch.int32, T * k, dev)
     for t, name in ((weights, "weights"), (dweights, "dweights")):
         _flat(t, name, torch.float32, T * k, dev)
-    dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev) if dlogits is None else dlogits
-    ld_d = _matrix(dlogits, "dlogits", T, E, dev, logits.dtype)
+    if dlogits is None:
+        dlogits, ld_d = torch.empty_like(logits), E
+    else:
+        ld_d = _matrix(dlogits, "dlogits", T, E, dev, logits.dtype)
     _launch(dev, _lib().mx_moe_route_backward, dweights.data_ptr(), logits.data_ptr(), logits.dtype is torch.float32, ld, T,
             E, k, bool(renormalize), experts.data_ptr(), weights.data_ptr(), dlogits.data_ptr(), ld_d)
     return dlogits
@@ -276,8 +287,8 @@ def mx_moe_sort(experts, num_experts, offsets=None, row_token=None, row_of=None,
     token): a MoERows.  An id outside [0, num_experts) has no row."""
     T, k, dev = _first(experts, "experts")
     _flat(experts, "experts", torch.int32, T * k, dev)
-    offsets, row_token, row_of = _rows_out(T, num_experts, k, dev, offsets, row_token, row_of)
-    workspace, have = _workspace(_lib().mx_moe_workspace(T, num_experts, k), workspace, dev)
+    offsets, row_token, row_of = _rows_out(T, num_experts, k, experts, offsets, row_token, row_of)
+    workspace, have = _workspace(_lib().mx_moe_workspace(T, num_experts, k), workspace, experts)
     _launch(dev, _lib().mx_moe_sort, experts.data_ptr(), T, num_experts, k, offsets.data_ptr(), row_token.data_ptr(),
             row_of.data_ptr(), _p(workspace), have)
     return MoERows(offsets, row_token, row_of)
@@ -301,7 +312,7 @@ def mx_moe_dispatch(x, row_of, num_rows=None, out=None):
     _, k = _row_of(row_of, T, dev)
     if num_rows is None:
         num_rows = T * k if out is None else out.shape[0]
-    out = torch.empty((num_rows, cols), dtype=torch.bfloat16, device=dev) if out is None else out
+    out = x.new_empty((num_rows, cols)) if out is None else out
     ld_out = _matrix(out, "out", num_rows, cols, dev)
     _launch(dev, _lib().mx_moe_dispatch, x.data_ptr(), ld_x, T, cols, row_of.data_ptr(), k, out.data_ptr(), ld_out, num_rows)
     return out
@@ -317,7 +328,7 @@ def mx_moe_combine(rows, row_of, weights=None, out=None):
     T, k = _row_of(row_of, None, dev)
     if weights is not None:
         _flat(weights, "weights", torch.float32, T * k, dev)
-    out = torch.empty((T, cols), dtype=torch.bfloat16, device=dev) if out is None else out
+    out = rows.new_empty((T, cols)) if out is None else out
     ld_out = _matrix(out, "out", T, cols, dev)
     _launch(dev, _lib().mx_moe_combine, rows.data_ptr(), ld_rows, M, row_of.data_ptr(), _p(weights), T, cols, k,
             out.data_ptr(), ld_out)
@@ -335,9 +346,9 @@ def mx_moe_combine_backward(dout, rows, row_of, weights, drows=None, dweights=No
     ld_rows = _matrix(rows, "rows", M, cols, dev)
     _, k = _row_of(row_of, T, dev)
     _flat(weights, "weights", torch.float32, T * k, dev)
-    drows = torch.empty((M, cols), dtype=torch.bfloat16, device=dev) if drows is None else drows
+    drows = rows.new_empty((M, cols)) if drows is None else drows
     ld_dr = _matrix(drows, "drows", M, cols, dev)
-    dweights = torch.empty((T, k), dtype=torch.float32, device=dev) if dweights is None else dweights
+    dweights = torch.empty_like(weights) if dweights is None else dweights
     _flat(dweights, "dweights", torch.float32, T * k, dev)
     _launch(dev, _lib().mx_moe_combine_backward, dout.data_ptr(), ld_d, rows.data_ptr(), ld_rows, M, row_of.data_ptr(),
             weights.data_ptr(), T, cols, k, drows.data_ptr(), ld_dr, dweights.data_ptr())
@@ -366,17 +377,18 @@ def nvfp4_rope_append(q, k, v, cache, block_table, seq_lens, inv_freq, q_offsets
     if not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be contiguous")
     if out is None:
-        out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((T, hq, d))
         ot, oh = hq * d, d
     else:
         _, ot, oh = _check_rows(out, "out", hq, d, T, dev)
     if with_dq or k_dq is not None or v_dq is not None:
-        k_dq = torch.empty((T, h, d), dtype=torch.bfloat16, device=dev) if k_dq is None else k_dq
-        v_dq = torch.empty((T, h, d), dtype=torch.bfloat16, device=dev) if v_dq is None else v_dq
         for name, t in (("k_dq", k_dq), ("v_dq", v_dq)):
-            _check_rows(t, name, h, d, T, dev)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+            if t is not None:
+                _check_rows(t, name, h, d, T, dev)
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+        k_dq = k.new_empty((T, h, d)) if k_dq is None else k_dq
+        v_dq = v.new_empty((T, h, d)) if v_dq is None else v_dq
     _launch(dev, _lib().nvfp4_rope_append, q.data_ptr(), qt, qh, hq, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, T,
             cache._ref, block_table.data_ptr(), ld, width, seq_lens.data_ptr(), _p(q_offsets), n, inv_freq.data_ptr(),
             2 * inv_freq.numel(), bool(interleaved), factor, out.data_ptr(), ot, oh, _p(k_dq), _p(v_dq))
