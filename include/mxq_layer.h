@@ -49,7 +49,7 @@ extern "C" {
  * NaN (or 0 where a finite value meets an infinite sum); its codes and scales are then unspecified.
  */
 mxq_status mx_rmsnorm(const uint16_t* x, int64_t ld_x, const uint16_t* residual, int64_t ld_r,
-                      const uint16_t* weight, int64_t rows, int64_t cols, float eps, uint16_t* h, int64_t ld_h,
+                      const uint16_t* weight, int64_t rows, int64_t cols, double eps, uint16_t* h, int64_t ld_h,
                       uint16_t* y, int64_t ld_y, float* rstd, mxq_format fmt, mxq_scale_layout layout,
                       uint8_t* codes, int64_t ld_codes, void* scales, float* gscales, uint16_t* dq, int64_t ld_dq,
                       void* stream);

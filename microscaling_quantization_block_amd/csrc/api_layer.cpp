@@ -101,14 +101,14 @@ mxq_status check_rows_call(const char* fn, const mxq::MoeRowsArgs& a) {
 extern "C" {
 
 mxq_status mx_rmsnorm(const uint16_t* x, int64_t ld_x, const uint16_t* residual, int64_t ld_r,
-                      const uint16_t* weight, int64_t rows, int64_t cols, float eps, uint16_t* h, int64_t ld_h,
+                      const uint16_t* weight, int64_t rows, int64_t cols, double eps, uint16_t* h, int64_t ld_h,
                       uint16_t* y, int64_t ld_y, float* rstd, mxq_format fmt, mxq_scale_layout layout,
                       uint8_t* codes, int64_t ld_codes, void* scales, float* gscales, uint16_t* dq, int64_t ld_dq,
                       void* stream) {
   const char* fn = "mx_rmsnorm";
   mxq_status s = check_norm_shape(fn, rows, cols);
   if (s != MXQ_OK) return s;
-  if (!(eps >= 0.0f) || !isfinite(eps)) return fail(MXQ_EINVAL, "%s: eps must be finite and not negative", fn);
+  if (!(eps >= 0.0) || !isfinite(eps)) return fail(MXQ_EINVAL, "%s: eps must be finite and not negative", fn);
   // the enumerators as numbers: a value the enum does not have must reach the checks
   const int f = static_cast<int>(fmt), lay = static_cast<int>(layout);
   const int64_t block = f == MXQ_FMT_MXFP8 ? 32 : f == MXQ_FMT_NVFP4 ? 16 : f == MXQ_FMT_BF16 ? 8 : 128;
@@ -220,6 +220,7 @@ int64_t mx_moe_workspace(int64_t tokens, int32_t num_experts, int32_t topk) {
     return 0;                                  // nothing to do, or refused
   mxq::MoeArgs a = {};
   a.T = tokens;
+  a.E = num_experts;
   a.k = topk;
   int64_t groups = 0;
   for (const bool routed : {false, true}) {

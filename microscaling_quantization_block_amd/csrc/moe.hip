@@ -192,10 +192,11 @@ __device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int6
   uint64_t* both = reinterpret_cast<uint64_t*>(lds);           // of all groups << 32 | of the groups before
   int* hist = sort_hist(lds, E);
 
-  // a lane adds eight experts' counts over every (THREADS / lanes of a row)-th
-  // group; the first eight of them are on their way while the workgroup's own
-  // slots are counted
-  const int per_row = (E + 7) / 8, slices = THREADS / per_row;
+  // a lane adds eight experts' counts over every slices-th group; the first eight
+  // of them are on their way while the workgroup's own slots are counted.  Not more
+  // slices than make 256 groups eight each: few experts would have many lanes add
+  // to the same place (8 experts, 8192 tokens: 10.0 us with 512 slices)
+  const int per_row = (E + 7) / 8, slices = min(THREADS / per_row, 32);
   const int col = threadIdx.x % per_row, slice = threadIdx.x / per_row;
   constexpr int AHEAD = 8;
   uint4 ahead[AHEAD];
@@ -240,7 +241,7 @@ __device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int6
         pre[2 * i + 1] += hi & earlier;
       }
     };
-    if (slice < slices) {
+    if (slice < min((int64_t)slices, a.groups)) {
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) add(ahead[i], slice + (int64_t)i * slices);
 #pragma unroll 4
@@ -311,10 +312,12 @@ __device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int6
     if (r >= rows) a.row_token[r] = 0;
 }
 
-constexpr int ROUTE_THREADS = 512;
+// Threads of a workgroup of the router: 32 tokens of 16 lanes, or 16 tokens of a wave, in a pass.
+constexpr int route_threads(int lanes) { return lanes == 64 ? 1024 : 512; }
 
 template <int LANES, int VPL, bool F32>
-__global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a) {
+__global__ __launch_bounds__(route_threads(LANES)) void route_kernel(MoeArgs a) {
+  constexpr int ROUTE_THREADS = route_threads(LANES);
   extern __shared__ __align__(16) int lds[];
   for (int i = threadIdx.x; i < a.E; i += ROUTE_THREADS) lds[i] = 0;
   __syncthreads();
@@ -329,13 +332,13 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a) {
     a.counts[blockIdx.x * (int64_t)pad + i] = (uint16_t)(i < a.E ? lds[i] : 0);
 }
 
-// Tokens that one workgroup routes and sorts: their experts stay in LDS.
-constexpr int ONE_TOKENS = 64;
+// Tokens that one workgroup routes in a pass and sorts: their experts stay in LDS.
+constexpr int one_tokens(int lanes) { return 1024 / lanes; }
 
 template <int LANES, int VPL, bool F32>
 __global__ __launch_bounds__(1024) void route_one_kernel(MoeArgs a) {
   extern __shared__ __align__(16) int lds[];
-  __shared__ int ids[ONE_TOKENS * LANES];      // topk is at most LANES
+  __shared__ int ids[one_tokens(LANES) * LANES];         // topk is at most LANES
   int* hist = sort_hist(lds, a.E);
   for (int i = threadIdx.x; i < SORT_WAVES * a.E; i += 1024) hist[i] = 0;
   __syncthreads();
@@ -434,15 +437,18 @@ struct Lanes {
   static constexpr bool F32 = F32_;
 };
 
-// Calls f with a Lanes for E experts and k choices: 16 lanes a token up to 256 experts (four tokens a wave: for 128
-// experts a round is 50 instructions for all four), a wave beyond, and where 16 lanes cannot hold the choices.
+// Lanes of a token: 16 up to 128 experts (four tokens a wave), a wave beyond, and where 16 lanes cannot hold the
+// choices.  (256 experts, top 8, with 16 lanes of sixteen logits each: 12.2, 14.3 and 18.8 us for 64, 512 and 8192
+// tokens; with a wave of four: 9.4, 10.4 and 17.8.)
+int lanes_of(int E, int k) { return k <= 16 && E <= 128 ? 16 : 64; }
+
+// Calls f with a Lanes for E experts and k choices.
 template <bool F32, class F>
 hipError_t with_lanes(int E, int k, F&& f) {
-  if (k <= 16) {
+  if (lanes_of(E, k) == 16) {
     if (E <= 16) return f(Lanes<16, 1, F32>());
     if (E <= 64) return f(Lanes<16, 4, F32>());
-    if (E <= 128) return f(Lanes<16, 8, F32>());
-    if (E <= 256) return f(Lanes<16, 16, F32>());
+    return f(Lanes<16, 8, F32>());
   }
   if (E <= 256) return f(Lanes<64, 4, F32>());
   if (E <= 512) return f(Lanes<64, 8, F32>());
@@ -458,11 +464,12 @@ hipError_t with_lanes(bool f32, int E, int k, F&& f) {
 void plan_moe(MoeArgs& a, bool routed) {
   a.groups = 0;
   a.group_tokens = a.T;
-  // one workgroup routes 64 tokens in a pass, or sorts a few thousand slots
-  if (routed ? a.T <= ONE_TOKENS : a.T * a.k <= 4096) return;
-  // 32 tokens are one pass of a workgroup of the router; up to 256 groups beyond that, while counts fit 16 bits
+  const int lanes = lanes_of(a.E, a.k);
+  if (routed ? a.T <= one_tokens(lanes) : a.T * a.k <= 4096) return;
+  // at least a pass of the router's workgroup; up to 256 groups beyond that, while counts fit 16 bits
+  const int64_t pass = routed ? route_threads(lanes) / lanes : 32;
   int64_t each = (a.T + 255) / 256;
-  each = each < 32 ? 32 : each;
+  each = each < pass ? pass : each;
   const int64_t most = 65535 / a.k;
   a.group_tokens = each < most ? each : most;
   a.groups = (a.T + a.group_tokens - 1) / a.group_tokens;
@@ -474,8 +481,8 @@ hipError_t launch_moe_route(const MoeArgs& a, hipStream_t st) {
     if (!a.groups)
       hipLaunchKernelGGL((route_one_kernel<W::LANES, W::VPL, W::F32>), dim3(1), dim3(1024), sort_lds(a.E), st, a);
     else
-      hipLaunchKernelGGL((route_kernel<W::LANES, W::VPL, W::F32>), dim3((unsigned)a.groups), dim3(ROUTE_THREADS), (size_t)a.E * 4,
-                         st, a);
+      hipLaunchKernelGGL((route_kernel<W::LANES, W::VPL, W::F32>), dim3((unsigned)a.groups),
+                         dim3(route_threads(W::LANES)), (size_t)a.E * 4, st, a);
     return hipGetLastError();
   });
   if (e != hipSuccess || !a.groups) return e;

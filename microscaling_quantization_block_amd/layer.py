@@ -27,8 +27,8 @@ def _lib():
     global _fns
     if _fns is None:
         L = lib()
-        i64, i32, vp, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
-        L.mx_rmsnorm.argtypes = [vp, i64, vp, i64, vp, i64, i64, f32, vp, i64, vp, i64, vp, i32, i32, vp, i64, vp, vp, vp,
+        i64, i32, vp, f64 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_double
+        L.mx_rmsnorm.argtypes = [vp, i64, vp, i64, vp, i64, i64, f64, vp, i64, vp, i64, vp, i32, i32, vp, i64, vp, vp, vp,
                                  i64, vp]
         L.mx_rmsnorm_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, vp, i64, vp, vp, i64, vp]
         L.mx_rmsnorm_backward_workspace.argtypes = [i64, i64]
@@ -40,7 +40,7 @@ def _lib():
         L.mx_moe_combine.argtypes = [vp, i64, i64, vp, vp, i64, i64, i32, vp, i64, vp]
         L.mx_moe_combine_backward.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, i64, i32, vp, i64, vp, vp]
         L.nvfp4_rope_append.argtypes = [vp, i64, i64, i32, vp, i64, i64, vp, i64, i64, i64, ctypes.POINTER(_Cache), vp, i64,
-                                        i64, vp, vp, i64, vp, i32, i32, ctypes.c_double, vp, i64, i64, vp, vp, vp]
+                                        i64, vp, vp, i64, vp, i32, i32, f64, vp, i64, i64, vp, vp, vp]
         for f in ("nvfp4_rope_append", "mx_rmsnorm", "mx_rmsnorm_backward", "mx_moe_route", "mx_moe_route_backward", "mx_moe_sort",
                   "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_backward"):
             getattr(L, f).restype = ctypes.c_int
@@ -311,7 +311,7 @@ def mx_moe_dispatch(x, row_of, num_rows=None, out=None):
     ld_x = _matrix(x, "x", T, cols, dev)
     _, k = _row_of(row_of, T, dev)
     if num_rows is None:
-        num_rows = T * k if out is None else out.shape[0]
+        num_rows = out.shape[0] if isinstance(out, torch.Tensor) and out.dim() else T * k
     out = x.new_empty((num_rows, cols)) if out is None else out
     ld_out = _matrix(out, "out", num_rows, cols, dev)
     _launch(dev, _lib().mx_moe_dispatch, x.data_ptr(), ld_x, T, cols, row_of.data_ptr(), k, out.data_ptr(), ld_out, num_rows)

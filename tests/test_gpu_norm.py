@@ -189,6 +189,16 @@ def test_magnitudes():
             assert torch.equal(a.codes[ok], b.codes[ok]) and torch.equal(a.scales[ok], b.scales[ok])
 
 
+@pytest.mark.parametrize("eps", [1e-5, 1.1e-12, 0.3, 7e-40])
+def test_eps_is_binary64(eps):
+    """Rows so small that eps, which binary32 would round by up to 2^-25 of itself or lose, makes rstd."""
+    m, rng = _m(), np.random.default_rng(14)
+    x = rng.standard_normal((4, 264)) * np.array([0.0, 1e-3, 1e-1, 1.0])[:, None] * eps ** 0.5
+    bits, w = F.bf16_rne(x), R.bf16(rng, 264)
+    say(f"norm eps {eps}")
+    _check_y(m.mx_rmsnorm(to_dev_bf16(bits), to_dev_bf16(w), eps, with_rstd=True), bits, w, None, eps)
+
+
 # ------------------------------------------------------------------- gradient
 
 def _backward_inputs(rng, rows, cols, dres):
