@@ -11,7 +11,11 @@
 // with the bytes that they give for y.
 //
 // Both kernels are bound by memory: a row is read once and stays in registers (a lane owns
-// chunks of eight values, 16 bytes), every output leaves from there.
+// chunks of eight values, 16 bytes), every output leaves from there.  8192 rows of 4096
+// with a residual, MXFP8 and its values: 303 MB in 55.8 us, 5.4 TB/s, where a large copy has
+// 5.2; 32001 rows, NVFP4: 213 us; one row 2.6 us, of which a launch alone is about 2.
+// What the backward reads much later (h, the codes' values) and dx go past the caches
+// (that alone: MXFP8 62.4 -> 55.8 us, the gradient of 32768 rows 216.8 -> 200).
 
 #include "lanes.h"
 #include "layer_kernels.h"
@@ -76,6 +80,10 @@ __device__ __forceinline__ uint4 fp8_values8(uint2 codes, uint32_t s) {
 
 // LANES lanes (16 or 64) times WAVES waves hold a row, CH chunks a lane: chunk
 // lane + LANES (wave CH + i).  16 lanes hold a short row of one chunk a lane, four rows a wave.
+// A wave a row needs no barrier and wins with many rows (32768 of 1024 values, NVFP4:
+// 55.7 us, 110.3 with four waves); more waves a row win with few (1100 of 4096, MXFP8: 10.9
+// against 13.1) and with long ones, where two chunks a lane leave registers for four waves
+// a SIMD (4096 rows of 16384, MXFP8: 109 us, 127 with eight chunks).
 template <int LANES, int WAVES, int CH, int FMT>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(NormArgs a) {
   static_assert(LANES == 64 || (LANES == 16 && WAVES == 1 && CH == 1), "rows of 16 lanes are short");
@@ -244,7 +252,9 @@ hipError_t launch_rmsnorm(const NormArgs& a, mxq_format fmt, hipStream_t st) {
 // The row sum and dw are binary32.  TEAMS teams of WAVES waves hold a row each;
 // a workgroup walks rows and keeps dw of its columns in registers; the teams'
 // sums meet in LDS, the workgroup's go to the workspace, and a second kernel adds those,
-// always in the same order (no atomics).
+// always in the same order (no atomics).  32768 rows of 4096 with dres: 1.07 GB in
+// 186 us, 5.8 TB/s, 199.7 with one team a workgroup and 1024 workgroups; 1003 rows of 2048:
+// 8.5 us, two launches (11.8 with a workgroup a row).
 
 namespace {
 

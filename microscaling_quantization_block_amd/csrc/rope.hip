@@ -10,8 +10,11 @@
 // A wave holds one token, or a share of its heads: it finds the token's request,
 // position and page once, a lane computes one angle, and the lanes then keep the eight
 // cosines and sines of their place in a row for all heads.  D / 8 lanes hold a row;
-// a half layout's partner values come from another lane of the row.  Bound by
-// memory for prompts, by one chain of latencies for a decode step.
+// a half layout's partner values come from another lane of the row.  Prompts are bound by
+// memory: 9.7 k tokens of 32 + 16 heads of 128, 250 MB in 49.1 us, 5.1 TB/s; a decode
+// step by one chain of latencies: 128 tokens 4.5 us (a launch alone is about 2).  The heads
+// are loaded before the token's request and page are looked up; behind the look-ups, and
+// with the source of a row chosen among kernel arguments, prompts took 60 us.
 
 #include "cache_device.h"
 #include "layer_kernels.h"
