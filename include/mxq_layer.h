@@ -106,7 +106,7 @@ int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
  * has no gradient.
  *
  * Sizes: num_experts up to 1024, topk up to 64 and num_experts; tokens below
- * 2^24, tokens * topk up to 2^26.  tokens == 0 gives offsets of zeros.
+ * 2^24, tokens * topk below 2^26.  tokens == 0 gives offsets of zeros.
  */
 mxq_status mx_moe_route(const void* logits, int32_t logits_f32, int64_t ld, int64_t tokens, int32_t num_experts,
                         int32_t topk, int32_t renormalize, int32_t* experts, float* weights, int32_t* offsets,
@@ -168,7 +168,8 @@ mxq_status mx_moe_combine_backward(const uint16_t* dout, int64_t ld_dout, const 
  *                 may be q itself, with its strides.  Rows of no request are not written.
  *   inv_freq      binary32 [rotary_dim / 2], on the device; p inv_freq[i] below 2^40
  *   rotary_dim    a multiple of 16, up to head_dim
- * Any positive num_q_heads: q and the cache need not belong to one attention.
+ * Any num_q_heads from 1 to 32767: q and the cache need not belong to one attention.
+ * tokens below 2^25.
  */
 mxq_status nvfp4_rope_append(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int32_t num_q_heads,
                              const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,

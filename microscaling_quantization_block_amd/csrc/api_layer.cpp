@@ -40,8 +40,8 @@ mxq_status check_norm_shape(const char* fn, int64_t rows, int64_t cols) {
 mxq_status check_slots(const char* fn, int64_t tokens, int topk) {
   if (tokens < 0) return fail(MXQ_EINVAL, "%s: negative size", fn);
   if (topk < 1 || topk > mxq::MOE_TOPK) return fail(MXQ_EINVAL, "%s: topk must be 1 to %d (topk=%d)", fn, mxq::MOE_TOPK, topk);
-  if (tokens >= (1 << 24) || tokens * topk > (1 << 26))
-    return fail(MXQ_EUNSUPPORTED, "%s: too many tokens for one call (below 2^24, 2^26 slots)", fn);
+  if (tokens >= (1 << 24) || tokens * topk >= (1 << 26))       // 32-bit grids: a wave per slot
+    return fail(MXQ_EUNSUPPORTED, "%s: too many tokens for one call (below 2^24, below 2^26 slots)", fn);
   return MXQ_OK;
 }
 
@@ -404,7 +404,7 @@ mxq_status nvfp4_rope_append(const uint16_t* q, int64_t q_token_stride, int64_t 
   if (!inv_freq) return fail(MXQ_EINVAL, "%s: inv_freq is NULL", fn);
   if (!aligned(inv_freq, 4)) return fail(MXQ_EALIGN, "%s: inv_freq 4-byte aligned", fn);
   if (!aligned16(k_dq) || !aligned16(v_dq)) return fail(MXQ_EALIGN, "%s: k_dq and v_dq 16-byte aligned", fn);
-  if (tokens >= (1 << 26)) return fail(MXQ_EUNSUPPORTED, "%s: too many rows for one call", fn);    // 32-bit grid
+  if (tokens >= (1 << 25)) return fail(MXQ_EUNSUPPORTED, "%s: too many rows for one call", fn);    // 32-bit grid
   a.p.k = k;
   a.p.v = v;
   a.p.T = tokens;

@@ -156,6 +156,39 @@ def test_captured_step():
         assert torch.equal(s.cache.k_codes, eager.cache.k_codes) and torch.equal(s.cache.v_scales, eager.cache.v_scales)
 
 
+@pytest.mark.parametrize("fmt,layout", [("NVFP4", "MFMA"), ("NVFP4", "LINEAR"), ("MXFP8", "MFMA")])
+def test_norm_feeds_the_products(fmt, layout):
+    """The norm's codes as an operand of mx_gemm, and of the experts' grouped gate_up product with the router's rows: the
+    bits of the norm and the quantizer called one by one."""
+    m, rng = _m(), np.random.default_rng(10)
+    T, H, N, EX, k = 96, 256, 128, 8, 2
+    x, r = (to_dev_bf16(R.bf16(rng, (T, H))) for _ in range(2))
+    w = to_dev_bf16(F.bf16_rne(1 + 0.1 * rng.standard_normal(H)))
+    fm, lay = m.Format[fmt], m.Layout[layout]
+    gs = m.GScale.PER_ROW if fmt == "NVFP4" else m.GScale.NONE
+    say(f"norm to product {fmt} {layout}")
+    n = m.mx_rmsnorm(x, w, EPS, residual=r, fmt=fm, layout=lay)
+    y = m.mx_rmsnorm(x, w, EPS, residual=r).y
+    q = (m.nvfp4_quantize(y, layout=lay) if fmt == "NVFP4" else m.mx_quantize(y, layout=lay)) + (None,)
+    fused, apart = (m.Operand(fm, c, s, g, gs=gs, layout=lay) for c, s, g in ((n.codes, n.scales, n.gscales), q[:3]))
+    wb = to_dev_bf16(R.bf16(rng, (N, H), 0.02))
+    if fmt == "NVFP4":
+        b = m.Operand(fm, *m.nvfp4_quantize(wb, gs=m.GScale.PER_TENSOR), gs=m.GScale.PER_TENSOR)
+    else:
+        b = m.Operand(fm, *m.mx_quantize(wb))
+    assert torch.equal(m.mx_gemm(fused, b, T, N, H), m.mx_gemm(apart, b, T, N, H))
+    if fmt != "NVFP4":
+        return
+    gate_up = D.Weight(rng, N, H, groups=EX).operand(m, torch)
+    rt = m.mx_moe_route(torch.from_numpy(rng.standard_normal((T, EX)).astype(np.float32)).cuda(), k)
+    kw = dict(group_row_offsets=rt.offsets, a_row_index=rt.row_token, a_rows=T)
+    h = [m.mx_gemm_swiglu(a, gate_up, T * k, N // 2, H, **kw) for a in (fused, apart)]
+    assert torch.equal(*h)
+    out = m.mx_moe_combine(h[0], rt.row_of, rt.weights)
+    ref, tol = R.combine_ref(_f64(h[0]), to_np(rt.row_of), to_np(rt.weights).astype(np.float64))
+    assert (np.abs(_f64(out) - ref) <= tol).all()
+
+
 def test_gradients_of_the_chain():
     """norm -> router and dispatched rows -> one product per expert (BF16 mx_gemm) -> combine, and back to the norm's input, its
     weight and the logits, against float64.  Seven BF16 roundings stand one behind the other, each at most 2^-8 of a value;

@@ -222,6 +222,27 @@ def test_rows_outside_and_strides():
     assert (none == 0).all()
 
 
+def test_rows_far_apart():
+    """Rows beyond 2^31 elements of their matrix."""
+    m = _m()
+    M, cols, T, k = 530_000, 4096, 40, 3
+    rows = torch.zeros((M, cols), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, dout = (torch.randn(T, cols, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w = torch.rand(T, k, generator=g, device="cuda")
+    row_of = (M - 1 - torch.randperm(T * k, generator=g, device="cuda")).int().view(T, k)
+    near = (row_of - (M - T * k)).contiguous()
+    say("far rows")
+    m.mx_moe_dispatch(x, row_of, out=rows)
+    small = m.mx_moe_dispatch(x, near)
+    assert torch.equal(rows[-T * k:], small) and not rows[:1000].any()
+    assert torch.equal(m.mx_moe_combine(rows, row_of, w), m.mx_moe_combine(small, near, w))
+    out = torch.zeros_like(rows)
+    _, dw = m.mx_moe_combine_backward(dout, rows, row_of, w, drows=out)
+    ds, dw2 = m.mx_moe_combine_backward(dout, small, near, w)
+    assert torch.equal(dw, dw2) and torch.equal(out[-T * k:], ds) and not out[:1000].any()
+
+
 def test_masked_rows_may_hold_anything():
     """A NaN in a row of no slot, and in the rows of a slot that is not there, reaches nothing."""
     m, rng = _m(), np.random.default_rng(13)

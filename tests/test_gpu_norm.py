@@ -137,6 +137,61 @@ def test_same_bits_for_any_number_of_rows(cols):
                 assert a is None or torch.equal(a[lo:hi], b), (fmt, name, lo)
 
 
+@pytest.mark.parametrize("rows,cols", [(33000, 128), (8300, 640), (8300, 2048), (8300, 4096), (2000, 4096), (2100, 8192),
+                                       (1100, 16384), (600, 32768)])
+@pytest.mark.parametrize("fmt", ["BF16", "NVFP4", "FP8_B128_F32"])
+def test_more_rows_than_workgroups(rows, cols, fmt):
+    """A workgroup walks several rows: they equal the rows in calls of few."""
+    m, rng = _m(), np.random.default_rng(rows)
+    fm = m.Format[fmt]
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x, r = (torch.randn(rows, cols, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w = to_dev_bf16(F.bf16_rne(1 + 0.1 * rng.standard_normal(cols)))
+    say(f"norm walks {rows}x{cols} {fmt}")
+    kw = dict(fmt=fm, with_rstd=True, with_y=True, with_dq=fm != m.Format.BF16)
+    full = m.mx_rmsnorm(x, w, EPS, residual=r, **kw)
+    for lo in (0, rows // 2 - 3, rows - 40):
+        part = m.mx_rmsnorm(x[lo:lo + 40], w, EPS, residual=r[lo:lo + 40], **kw)
+        for a, b in zip(full, part):
+            assert (a is None) == (b is None) and (a is None or torch.equal(a[lo:lo + 40], b)), lo
+
+
+def test_rows_far_apart():
+    """Rows beyond 2^31 elements of their matrix, in both directions."""
+    m = _m()
+    rows, cols = 530_000, 4096
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    tail = torch.randn(50, cols, generator=g, device="cuda").to(torch.bfloat16)
+    x[-50:] = tail
+    w = torch.full((cols,), 1.5, dtype=torch.bfloat16, device="cuda")
+    say("far rows")
+    n = m.mx_rmsnorm(x, w, EPS, residual=x, h=x, with_rstd=True)
+    want = m.mx_rmsnorm(tail, w, EPS, residual=tail, with_rstd=True)
+    assert torch.equal(n.y[-50:], want.y) and torch.equal(x[-50:], want.h) and torch.equal(n.rstd[-50:], want.rstd)
+    assert not n.y[:1000].any()
+    dx, dw = m.mx_rmsnorm_backward(n.y, x, w, n.rstd)
+    small, dw2 = m.mx_rmsnorm_backward(want.y, want.h, w, want.rstd)
+    assert torch.equal(dx[-50:], small) and not dx[:1000].any()
+    # the rows of zeros add nothing; the others' order differs
+    bound = 54 * 2 * R.EPS_F32 * (want.y.double() * want.h.double() * want.rstd[:, None]).abs().sum(0)
+    assert ((dw - dw2).abs() <= 2 * bound).all()
+
+
+def test_padded_inputs_and_new_outputs():
+    m, rng = _m(), np.random.default_rng(19)
+    x, w, r = (to_dev_bf16(t) for t in _inputs(rng, 21, 256, True))
+    pad = lambda t: torch.nn.functional.pad(t, (0, 40))[:, :256]
+    say("padded inputs")
+    a, b = m.mx_rmsnorm(x, w, EPS, residual=r, with_rstd=True), m.mx_rmsnorm(pad(x), w, EPS, residual=pad(r), with_rstd=True)
+    assert torch.equal(a.y, b.y) and torch.equal(a.h, b.h) and b.y.is_contiguous() and b.h.is_contiguous()
+    for k in range(2):                                     # one row, of any stride
+        one = m.mx_rmsnorm(pad(x)[k:k + 1], w, EPS, residual=r[k:k + 1])
+        assert torch.equal(one.y, a.y[k:k + 1])
+    u, v = (m.mx_rmsnorm_backward(f(x), f(a.h), w, a.rstd, dresidual=f(r)) for f in (lambda t: t, pad))
+    assert torch.equal(u[0], v[0]) and torch.equal(u[1], v[1])
+
+
 def test_strides_and_in_place():
     m, rng = _m(), np.random.default_rng(9)
     rows, cols = 37, 520
@@ -228,7 +283,8 @@ def test_backward(rows, cols, dres):
     assert none is None and torch.equal(alone, dx)
 
 
-@pytest.mark.parametrize("rows,cols", [(1030, 512), (2500, 136), (1500, 4096), (700, 8192), (300, 20000)])
+@pytest.mark.parametrize("rows,cols", [(1030, 512), (2500, 136), (5000, 264), (2100, 1032), (1500, 4096), (700, 8192),
+                                       (600, 12296), (300, 20000)])
 def test_backward_many_rows(rows, cols):
     """More rows than workgroups: each walks several; dw has many partial sums."""
     m, rng = _m(), np.random.default_rng(rows)
@@ -284,6 +340,19 @@ def test_backward_in_place_and_empty():
     assert dx.shape == (0, 264) and (dw == 0).all()
     n = m.mx_rmsnorm(none, wd, EPS, residual=none, fmt=m.Format.BF16, with_rstd=True)
     assert n.y.shape == (0, 264)
+
+
+@pytest.mark.parametrize("cols", [1032, 4096, 8200, 20000])
+def test_backward_in_place_wide(cols):
+    m, rng = _m(), np.random.default_rng(cols)
+    h, w, dy, rstd, dr = _backward_inputs(rng, 9, cols, True)
+    hd, wd, rd = to_dev_bf16(h), to_dev_bf16(w), torch.from_numpy(rstd).cuda()
+    say(f"norm backward in place {cols}")
+    want, dw = m.mx_rmsnorm_backward(to_dev_bf16(dy), hd, wd, rd, dresidual=to_dev_bf16(dr))
+    for over in (0, 1):
+        a, b = to_dev_bf16(dy), to_dev_bf16(dr)
+        dx, dw2 = m.mx_rmsnorm_backward(a, hd, wd, rd, dresidual=b, dx=(a, b)[over])
+        assert torch.equal(dx, want) and torch.equal(dw2, dw)
 
 
 def test_spoilt_rows_of_the_gradient():

@@ -134,7 +134,8 @@ def test_route_and_sort_reject_bad_arguments():
         assert route(**kw) == EALIGN, kw
     for kw in (dict(ids=two), dict(tok=two), dict(row=two), dict(ws=ODD)):
         assert sort(**kw) == EALIGN, kw
-    for kw in (dict(E=1025, ld=1025), dict(T=1 << 24), dict(T=(1 << 24) - 1, k=5), dict(ld=1 << 31)):
+    for kw in (dict(E=1025, ld=1025), dict(T=1 << 24), dict(T=(1 << 24) - 1, k=5), dict(T=1 << 20, k=64, E=64, ld=64),
+               dict(ld=1 << 31)):
         assert route(**kw) == EUNSUPPORTED, kw
     for kw in (dict(E=1025), dict(T=1 << 24), dict(T=(1 << 24) - 1, k=5)):
         assert sort(**kw) == EUNSUPPORTED, kw
@@ -178,7 +179,7 @@ def test_rows_calls_reject_bad_arguments():
         for kw in (dict(rows=ODD), dict(ld=68), dict(ld_r=68), dict(row=two)):
             assert fn(**kw) == EALIGN, (fn, kw)
         assert fn(cols=60) == ESHAPE
-        for kw in (dict(T=1 << 24), dict(T=(1 << 24) - 1, k=5), dict(cols=1 << 26, ld=1 << 26, ld_r=1 << 26),
+        for kw in (dict(T=1 << 24), dict(T=(1 << 24) - 1, k=5), dict(T=1 << 20, k=64), dict(cols=1 << 26, ld=1 << 26, ld_r=1 << 26),
                    dict(M=1 << 31)):
             assert fn(**kw) == EUNSUPPORTED, (fn, kw)
         assert fn(T=0, row=None) == 0
@@ -223,7 +224,7 @@ def test_rope_append_rejects_bad_arguments():
     for kw in (dict(q=ODD), dict(k=ODD), dict(out=ODD), dict(vs=(256, 100)), dict(qs=(1020, 128)), dict(os_=(1024, 100)),
                dict(kd=ODD), dict(vd=ODD), dict(freq=ctypes.c_void_p(0x10002))):
         assert call(**kw) == EALIGN, kw
-    assert call(tokens=1 << 26, offs=FAKE) == EUNSUPPORTED and call(tokens=1 << 31, offs=FAKE) == EUNSUPPORTED
+    assert call(tokens=1 << 25, offs=FAKE) == EUNSUPPORTED and call(tokens=1 << 31, offs=FAKE) == EUNSUPPORTED
     assert call(tokens=0, n=0) == 0 and call(tokens=0, offs=FAKE) == 0
 
 
