@@ -46,7 +46,8 @@ extern "C" {
  * MFMA scales: rows % 32 == 0, cols a multiple of four blocks.
  * Alignment: 16 bytes, strides multiples of 16 bytes; rstd and gscales 4 bytes.
  * A row with an infinity or a NaN, or with eps 0 and nothing but zeros, becomes
- * NaN (or 0 where a finite value meets an infinite sum); its codes and scales are then unspecified.
+ * NaN (or 0 where a finite value meets an infinite sum); with eps 0, a row whose
+ * rstd is beyond binary32 becomes infinite.  Codes and scales of such a row are unspecified.
  */
 mxq_status mx_rmsnorm(const uint16_t* x, int64_t ld_x, const uint16_t* residual, int64_t ld_r,
                       const uint16_t* weight, int64_t rows, int64_t cols, double eps, uint16_t* h, int64_t ld_h,

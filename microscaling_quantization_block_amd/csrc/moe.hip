@@ -317,23 +317,25 @@ __device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int6
     if (r >= rows) a.row_token[r] = 0;
 }
 
-// Threads of a workgroup of the router: 32 tokens of 16 lanes, or 16 tokens of a wave, in a pass.
-constexpr int route_threads(int lanes) { return lanes == 64 ? 1024 : 512; }
+// Threads of a workgroup of the router that has `tokens` of `lanes` lanes: one pass
+// for 32 tokens of 16 lanes; more fill the workgroup (65536 tokens of 128 experts: 31.8 us
+// with 512 threads, 28.2 with 1024, the sort included).
+inline int route_threads(int lanes, int64_t tokens) { return lanes * tokens <= 512 ? 512 : 1024; }
 
 template <int LANES, int VPL, bool F32>
-__global__ __launch_bounds__(route_threads(LANES)) void route_kernel(MoeArgs a) {
-  constexpr int ROUTE_THREADS = route_threads(LANES);
+__global__ __launch_bounds__(1024) void route_kernel(MoeArgs a) {
   extern __shared__ __align__(16) int lds[];
-  for (int i = threadIdx.x; i < a.E; i += ROUTE_THREADS) lds[i] = 0;
+  const int threads = (int)blockDim.x;
+  for (int i = threadIdx.x; i < a.E; i += threads) lds[i] = 0;
   __syncthreads();
   const int64_t first = blockIdx.x * a.group_tokens, last = min(a.T, first + a.group_tokens);
-  for (int64_t t = first + threadIdx.x / LANES; t < last; t += ROUTE_THREADS / LANES)
+  for (int64_t t = first + threadIdx.x / LANES; t < last; t += threads / LANES)
     route_token<LANES, VPL, F32>(a, t, threadIdx.x & (LANES - 1), [&](int64_t, int e) {
       if (e >= 0) atomicAdd(&lds[e], 1);
     });
   __syncthreads();
   const int pad = (a.E + 7) / 8 * 8;
-  for (int i = threadIdx.x; i < pad; i += ROUTE_THREADS)
+  for (int i = threadIdx.x; i < pad; i += threads)
     a.counts[blockIdx.x * (int64_t)pad + i] = (uint16_t)(i < a.E ? lds[i] : 0);
 }
 
@@ -470,9 +472,10 @@ void plan_moe(MoeArgs& a, bool routed) {
   a.groups = 0;
   a.group_tokens = a.T;
   const int lanes = lanes_of(a.E, a.k);
-  if (routed ? a.T <= one_tokens(lanes) : a.T * a.k <= 4096) return;
+  // one workgroup routes its pass of tokens, or sorts some slots (512 slots 3.6 us, 4096 9.8, where two launches take 7.2)
+  if (routed ? a.T <= one_tokens(lanes) : a.T * a.k <= 2048) return;
   // at least a pass of the router's workgroup; up to 256 groups beyond that, while counts fit 16 bits
-  const int64_t pass = routed ? route_threads(lanes) / lanes : 32;
+  const int64_t pass = lanes == 16 ? 32 : 16;
   int64_t each = (a.T + 255) / 256;
   each = each < pass ? pass : each;
   const int64_t most = 65535 / a.k;
@@ -487,7 +490,7 @@ hipError_t launch_moe_route(const MoeArgs& a, hipStream_t st) {
       hipLaunchKernelGGL((route_one_kernel<W::LANES, W::VPL, W::F32>), dim3(1), dim3(1024), sort_lds(a.E), st, a);
     else
       hipLaunchKernelGGL((route_kernel<W::LANES, W::VPL, W::F32>), dim3((unsigned)a.groups),
-                         dim3(route_threads(W::LANES)), (size_t)a.E * 4, st, a);
+                         dim3((unsigned)route_threads(W::LANES, a.group_tokens)), (size_t)a.E * 4, st, a);
     return hipGetLastError();
   });
   if (e != hipSuccess || !a.groups) return e;

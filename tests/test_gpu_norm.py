@@ -215,10 +215,11 @@ def test_strides_and_in_place():
     assert torch.equal(codes[:, :256], plain.codes) and (codes[:, 256:] == 7).all()
 
 
-def test_magnitudes():
-    """Zeros, subnormals, the largest values (whose squares leave binary32), eps 0; spoilt rows leave the others."""
+@pytest.mark.parametrize("cols", [128, 640, 4096])
+def test_magnitudes(cols):
+    """Zeros, subnormals, the largest values (whose squares leave binary32), eps 0; spoilt rows leave the others.  Short
+    rows of all magnitudes share a wave."""
     m, rng = _m(), np.random.default_rng(4)
-    cols = 640
     x = rng.standard_normal((8, cols))
     x[1] = 0.0
     x[2] *= 2.0 ** 120
@@ -235,8 +236,12 @@ def test_magnitudes():
     spoilt = bits.copy()
     spoilt[1, 5] = 0x7F80
     spoilt[6, 7] = 0x7FC0
-    for fmt in (m.Format.BF16, m.Format.NVFP4, m.Format.MXFP8, m.Format.FP8_B128_F32):
-        a = m.mx_rmsnorm(to_dev_bf16(bits), to_dev_bf16(w), EPS, fmt=fmt, with_y=True)
+    for fmt in m.Format:
+        a = m.mx_rmsnorm(to_dev_bf16(bits), to_dev_bf16(w), EPS, fmt=fmt, with_y=True, with_dq=fmt != m.Format.BF16)
+        if fmt != m.Format.BF16:                           # the smallest and largest scales among them
+            c, s, S, dq = _quantized(m, fmt, m.Layout.LINEAR, from_dev_bf16(a.y))
+            assert np.array_equal(to_np(a.codes), c) and np.array_equal(from_dev_bf16(a.dq), dq)
+            assert np.array_equal(to_np(a.scales), s) and (S is None or np.array_equal(to_np(a.gscales), S))
         b = m.mx_rmsnorm(to_dev_bf16(spoilt), to_dev_bf16(w), EPS, fmt=fmt, with_y=True)
         ok = [0, 2, 3, 4, 5, 7]
         assert torch.equal(a.y[ok], b.y[ok]) and torch.isnan(b.y[6]).all() and torch.isnan(b.y[1, 5])
