@@ -44,7 +44,8 @@ extern "C" {
  *                   mx_dequantize gives them (not with MXQ_FMT_BF16)
  * Shapes: cols % 8 == 0, the format's block divides cols; cols up to 32768.
  * MFMA scales: rows % 32 == 0, cols a multiple of four blocks.
- * Alignment: 16 bytes, strides multiples of 16 bytes; rstd and gscales 4 bytes.
+ * Alignment: 16 bytes, strides multiples of 16 bytes (NVFP4 codes: of 8); rstd
+ * and gscales 4 bytes.
  * A row with an infinity or a NaN, or with eps 0 and nothing but zeros, becomes
  * NaN (or 0 where a finite value meets an infinite sum); with eps 0, a row whose
  * rstd is beyond binary32 becomes infinite.  Codes and scales of such a row are unspecified.

@@ -137,8 +137,10 @@ mxq_status mx_rmsnorm(const uint16_t* x, int64_t ld_x, const uint16_t* residual,
     if (f != MXQ_FMT_NVFP4 && gscales) return fail(MXQ_EINVAL, "%s: gscales are NVFP4's", fn);
     if (ld_codes < (f == MXQ_FMT_NVFP4 ? cols / 2 : cols))
       return fail(MXQ_EINVAL, "%s: leading dimension of the codes smaller than the row", fn);
-    if (!aligned16(codes) || ld_codes % 16 || !aligned(gscales, 4) || (f == MXQ_FMT_FP8_B128_F32 && !aligned(scales, 4)))
-      return fail(MXQ_EALIGN, "%s: codes 16-byte aligned, ld_codes %% 16 == 0, float scales 4-byte aligned", fn);
+    // a block of NVFP4 is 8 bytes (the quantizer's rule), of MXFP8 32; the kernel stores whole words
+    const int64_t unit = f == MXQ_FMT_NVFP4 ? 8 : 16;
+    if (!aligned16(codes) || ld_codes % unit || !aligned(gscales, 4) || (f == MXQ_FMT_FP8_B128_F32 && !aligned(scales, 4)))
+      return fail(MXQ_EALIGN, "%s: codes 16-byte aligned, ld_codes %% %d == 0, float scales 4-byte aligned", fn, (int)unit);
     if (dq && (s = check_matrix(fn, "dq", dq, ld_dq, cols)) != MXQ_OK) return s;
   }
 

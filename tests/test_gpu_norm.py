@@ -102,6 +102,25 @@ def test_quantized_output(fmt, rows, cols, layout):
     assert torch.equal(bare.codes, n.codes) and torch.equal(bare.scales, n.scales)
 
 
+# rows that end inside a lane group, a block's lanes or a wave: odd numbers of blocks
+NARROW = [(fmt, "LINEAR", rows, cols) for fmt, widths in (("NVFP4", (16, 48, 144, 272, 1040, 4112)), ("MXFP8", (32, 96, 160, 544, 4128)))
+          for cols in widths for rows in (1, 5, 32)] + [("NVFP4", "MFMA", 32, cols) for cols in (64, 192, 576)]
+
+
+@pytest.mark.parametrize("fmt,layout,rows,cols", NARROW)
+def test_quantized_output_of_any_whole_blocks(fmt, layout, rows, cols):
+    m, rng = _m(), np.random.default_rng(rows + cols)
+    fm, lay = m.Format[fmt], m.Layout[layout]
+    x, w, r = _inputs(rng, rows, cols, rows % 2 == 1)
+    say(f"norm {fmt} {layout} {rows}x{cols}, whole blocks")
+    n = m.mx_rmsnorm(to_dev_bf16(x), to_dev_bf16(w), EPS, residual=None if r is None else to_dev_bf16(r), fmt=fm, layout=lay,
+                     with_rstd=True, with_y=True, with_dq=True)
+    c, s, S, dq = _quantized(m, fm, lay, _check_y(n, x, w, r))
+    assert np.array_equal(to_np(n.codes), c) and np.array_equal(from_dev_bf16(n.dq), dq)
+    assert np.array_equal(to_np(n.scales).reshape(-1), np.ascontiguousarray(s).reshape(-1))
+    assert S is None or np.array_equal(to_np(n.gscales), S)
+
+
 def test_bytes_of_the_quantizers():
     """The fused copies are those of the library's own quantizers."""
     m, rng = _m(), np.random.default_rng(5)

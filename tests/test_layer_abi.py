@@ -78,6 +78,23 @@ def test_norm_rejects_bad_arguments():
     assert call(rows=0, x=None, y=None) == 0 and call(cols=0, x=None) == 0      # nothing to do, nothing launched
 
 
+def test_norm_takes_nvfp4_codes_of_any_whole_blocks():
+    """NVFP4 rows are 8 bytes a block, so a stride of 8 bytes is enough, as in nvfp4_quantize; the FP8 formats need 16.
+    The values' matrix is checked behind the codes: its status says that the codes passed."""
+    m, L = _lib()
+
+    def call(fmt, cols, ld_c):
+        nv = fmt == m.Format.NVFP4
+        return L.mx_rmsnorm(FAKE, cols, None, 0, FAKE, 4, cols, 1e-6, None, 0, None, 0, None, fmt, 0, FAKE, ld_c, FAKE,
+                            FAKE if nv else None, FAKE, cols - 8, None)
+
+    for cols in (16, 32, 48, 144, 272, 4112):
+        assert call(m.Format.NVFP4, cols, cols // 2) == EINVAL and "dq" in m.lib().mxq_last_error().decode(), cols
+        assert call(m.Format.NVFP4, cols, cols // 2 + 4) == EALIGN, cols
+    for cols in (32, 96, 160):
+        assert call(m.Format.MXFP8, cols, cols) == EINVAL and call(m.Format.MXFP8, cols, cols + 8) == EALIGN, cols
+
+
 def test_norm_backward_rejects_bad_arguments():
     m, L = _lib()
     big, need = 1 << 40, m.mx_rmsnorm_backward_workspace(5, 64)
