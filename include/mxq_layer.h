@@ -108,7 +108,7 @@ int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
  * has no gradient.
  *
  * Sizes: num_experts up to 1024, topk up to 64 and num_experts; tokens below
- * 2^24, tokens * topk below 2^26.  tokens == 0 gives offsets of zeros.
+ * 2^24, tokens * topk at most 2^26 - 4.  tokens == 0 gives offsets of zeros.
  */
 mxq_status mx_moe_route(const void* logits, int32_t logits_f32, int64_t ld, int64_t tokens, int32_t num_experts,
                         int32_t topk, int32_t renormalize, int32_t* experts, float* weights, int32_t* offsets,

@@ -40,8 +40,9 @@ mxq_status check_norm_shape(const char* fn, int64_t rows, int64_t cols) {
 mxq_status check_slots(const char* fn, int64_t tokens, int topk) {
   if (tokens < 0) return fail(MXQ_EINVAL, "%s: negative size", fn);
   if (topk < 1 || topk > mxq::MOE_TOPK) return fail(MXQ_EINVAL, "%s: topk must be 1 to %d (topk=%d)", fn, mxq::MOE_TOPK, topk);
-  if (tokens >= (1 << 24) || tokens * topk >= (1 << 26))       // 32-bit grids: a wave per slot
-    return fail(MXQ_EUNSUPPORTED, "%s: too many tokens for one call (below 2^24, below 2^26 slots)", fn);
+  // 32-bit grids: up to a workgroup of 256 lanes per token, one per four slots (rounded up)
+  if (tokens >= (1 << 24) || tokens * topk > (1 << 26) - 4)
+    return fail(MXQ_EUNSUPPORTED, "%s: too many tokens for one call (below 2^24, at most 2^26 - 4 slots)", fn);
   return MXQ_OK;
 }
 

@@ -309,7 +309,7 @@ __device__ __forceinline__ void sort_slots(const MoeArgs& a, int64_t group, int6
       if (s < to) {
         const int64_t slot = first + s;
         a.row_of[slot] = e < E ? at : -1;
-        if (e < E) a.row_token[at] = (int)((uint32_t)slot / (uint32_t)a.k);      // slots stay below 2^27
+        if (e < E) a.row_token[at] = (int)((uint32_t)slot / (uint32_t)a.k);      // slots stay below 2^26
       }
     }
   // rows of no slot: token 0, a row that a gather may read
@@ -602,7 +602,7 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeRowsArgs a, int lx) {
 __global__ __launch_bounds__(256) void combine_backward_kernel(MoeRowsArgs a) {
   const int lane = threadIdx.x & 63;
   const uint32_t s = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (s >= (uint32_t)(a.T * a.k)) return;      // whole waves leave; slots stay below 2^27
+  if (s >= (uint32_t)(a.T * a.k)) return;      // whole waves leave; slots stay below 2^26
   const int64_t t = s / (uint32_t)a.k, r = a.row_of[s];
   if (r < 0 || r >= a.M) {                     // no row, no gradient
     if (lane == 0) a.dweights[s] = 0.0f;

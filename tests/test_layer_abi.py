@@ -208,6 +208,30 @@ def test_rows_calls_reject_bad_arguments():
     assert combine(w=two) == EALIGN and dispatch(M=0) == 0 and dispatch(cols=0) == 0
 
 
+def test_slots_fill_a_32_bit_grid_at_most():
+    """A workgroup of 256 lanes takes four slots: 2^26 - 4 slots are 2^32 - 256 lanes, one more slot is a workgroup more.
+    A misaligned array stops the calls that pass the limit before anything is launched."""
+    m, L = _lib()
+    two, ws = ctypes.c_void_p(0x10002), 1 << 40
+    calls = {
+        "sort": lambda T, k: L.mx_moe_sort(two, T, 64, k, FAKE, FAKE, FAKE, FAKE, ws, None),
+        "route": lambda T, k: L.mx_moe_route(FAKE, 1, 64, T, 64, k, 1, two, FAKE, FAKE, FAKE, FAKE, FAKE, ws, None),
+        "route_backward": lambda T, k: L.mx_moe_route_backward(two, FAKE, 1, 64, T, 64, k, 1, FAKE, FAKE, FAKE, 64, None),
+        "dispatch": lambda T, k: L.mx_moe_dispatch(FAKE, 64, T, 64, two, k, FAKE, 64, 10, None),
+        "combine": lambda T, k: L.mx_moe_combine(FAKE, 64, 10, two, FAKE, T, 64, k, FAKE, 64, None),
+        "combine_backward": lambda T, k: L.mx_moe_combine_backward(FAKE, 64, FAKE, 64, 10, two, FAKE, T, 64, k, FAKE, 64, FAKE,
+                                                                   None),
+    }
+    most = (1 << 26) - 4
+    for name, call in calls.items():
+        for T, k in (((1 << 24) - 1, 4), (1 << 20, 63)):       # the limit itself, and below
+            assert T * k <= most and call(T, k) == EALIGN, (name, T, k)
+        # 2^26 - 3, 2^26 - 2 twice, 2^26 - 1, 2^26
+        for T, k in ((1813753, 37), (1082401, 62), (2164802, 31), (22369621, 3), (1 << 20, 64)):
+            assert T * k > most and call(T, k) == EUNSUPPORTED, (name, T, k)
+        assert "slots" in m.lib().mxq_last_error().decode()
+
+
 def test_moe_binding_refuses_before_the_library_is_called():
     m, _ = _lib()
     x, i = torch.zeros(4, 64), torch.zeros(4, 2, dtype=torch.int32)
