@@ -156,6 +156,48 @@ def test_same_bits_for_any_number_of_rows(cols):
                 assert a is None or torch.equal(a[lo:hi], b), (fmt, name, lo)
 
 
+# from 2048 rows on, 1025 to 4096 columns are a wave a row: whole and partial waves, every format and layout
+WAVE_A_ROW = [(fmt, "LINEAR", rows, cols) for rows, cols in ((2048, 2048), (2051, 1152), (2080, 2304), (2049, 4096))
+              for fmt in ("MXFP8", "NVFP4", "FP8_B128", "FP8_B128_F32")] + \
+             [(fmt, "MFMA", rows, cols) for rows, cols in ((2048, 2048), (2080, 1152), (2112, 2304), (2048, 4096))
+              for fmt in ("MXFP8", "NVFP4")]
+
+
+@pytest.mark.parametrize("fmt,layout,rows,cols", WAVE_A_ROW)
+def test_quantized_output_of_a_wave_a_row(fmt, layout, rows, cols):
+    """Every byte of a learner's batch against the oracle's quantizers of y."""
+    m, rng = _m(), np.random.default_rng(rows + cols)
+    fm, lay = m.Format[fmt], m.Layout[layout]
+    x, w, r = _inputs(rng, rows, cols, True)
+    x[0] = r[0] = x[rows - 1] = r[rows - 1] = 0            # rows of zeros
+    say(f"norm {fmt} {layout} {rows}x{cols}, a wave a row")
+    kw = dict(residual=to_dev_bf16(r), fmt=fm, layout=lay, with_rstd=True)
+    xd, wd = to_dev_bf16(x), to_dev_bf16(w)
+    n = m.mx_rmsnorm(xd, wd, EPS, with_y=True, with_dq=True, **kw)
+    c, s, S, dq = _quantized(m, fm, lay, _check_y(n, x, w, r))
+    assert np.array_equal(to_np(n.codes), c) and np.array_equal(from_dev_bf16(n.dq), dq)
+    assert np.array_equal(to_np(n.scales).reshape(-1), np.ascontiguousarray(s).reshape(-1))
+    assert S is None or np.array_equal(to_np(n.gscales), S)
+    bare = m.mx_rmsnorm(xd, wd, EPS, **kw)
+    assert torch.equal(bare.codes, n.codes) and torch.equal(bare.scales, n.scales) and torch.equal(bare.h, n.h)
+
+
+@pytest.mark.parametrize("cols", [1024, 1152, 2048, 2304, 4096])
+@pytest.mark.parametrize("fmt", ["BF16", "MXFP8", "NVFP4", "FP8_B128", "FP8_B128_F32"])
+def test_same_bits_below_and_from_2048_rows(cols, fmt):
+    """The kernels that share a row among four waves (2047 rows and fewer) and that give it one (2048 and more) agree."""
+    m, rng = _m(), np.random.default_rng(cols)
+    fm = m.Format[fmt]
+    x, w, r = (to_dev_bf16(t) for t in _inputs(rng, 2100, cols, True))
+    say(f"norm {fmt} of 2100 rows and fewer, {cols}")
+    kw = dict(fmt=fm, with_rstd=True, with_y=True, with_dq=fm != m.Format.BF16)
+    full = m.mx_rmsnorm(x, w, EPS, residual=r, **kw)
+    for lo, hi in ((0, 1), (0, 2047), (52, 2100), (53, 2100), (2099, 2100)):
+        part = m.mx_rmsnorm(x[lo:hi], w, EPS, residual=r[lo:hi], **kw)
+        for name, a, b in zip(full._fields, full, part):
+            assert (a is None) == (b is None) and (a is None or torch.equal(a[lo:hi], b)), (name, lo, hi)
+
+
 @pytest.mark.parametrize("rows,cols", [(33000, 128), (8300, 640), (8300, 2048), (8300, 4096), (2000, 4096), (2100, 8192),
                                        (1100, 16384), (600, 32768)])
 @pytest.mark.parametrize("fmt", ["BF16", "NVFP4", "FP8_B128_F32"])
