@@ -136,6 +136,45 @@ def test_sort(T, E, k):
         _check_rows(got, ids, E)
 
 
+@pytest.mark.parametrize("T,E,k", [(65, 9, 1), (16, 128, 8), (43, 128, 8), (64, 128, 8), (100, 40, 10), (128, 1024, 16),
+                                   (2047, 1000, 1), (2048, 3, 1), (256, 128, 8), (2049, 3, 1), (205, 33, 10)])
+def test_sort_by_one_workgroup(T, E, k):
+    """64 to 2048 slots, one workgroup whose waves have one to four pieces of 64 each, and the first sizes beyond."""
+    m, rng = _m(), np.random.default_rng(T + E + k)
+    for kind in ("any", "last", "outside"):
+        ids = rng.integers(0, E, (T, k)).astype(np.int32)
+        if kind == "last":
+            ids[:] = E - 1
+        if kind == "outside":
+            ids[rng.random((T, k)) < 0.5] = -1
+            ids[0, 0], ids[-1, -1] = E, -2147483648
+        say(f"sort by one workgroup T {T} E {E} k {k} {kind}")
+        _check_rows(m.mx_moe_sort(torch.from_numpy(ids).cuda(), E), ids, E)
+
+
+# groups of more tokens than their workgroup routes at once: beyond 16384 tokens of 16 lanes, 4096 of a wave; the last
+# pass of a group is a partial one
+@pytest.mark.parametrize("T,E,k", [(17000, 16, 2), (40000, 60, 4), (20000, 128, 8), (5000, 200, 6), (4500, 100, 20),
+                                   (9000, 512, 10), (4200, 1000, 33)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_route_in_several_passes(T, E, k, dtype):
+    m, rng = _m(), np.random.default_rng(T + E)
+    x, xd = _logits(rng, T, E, dtype, "masked")
+    dw = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+    for renorm in (True, False):
+        say(f"route in passes T {T} E {E} k {k} {dtype} renorm {renorm}")
+        r = m.mx_moe_route(xd, k, renormalize=renorm)
+        ids, w, tol = R.route_ref(x, k, renorm)
+        assert np.array_equal(to_np(r.experts), ids)
+        assert (np.abs(to_np(r.weights) - w) <= tol).all()
+        _check_rows(r, ids, E)
+        # a token's gradient is the same in a call of few
+        d = m.mx_moe_route_backward(dw, xd, r.experts, r.weights, renormalize=renorm)
+        for lo, hi in ((0, 40), (T // 2 - 20, T // 2 + 20), (T - 33, T)):
+            part = m.mx_moe_route_backward(dw[lo:hi], xd[lo:hi], r.experts[lo:hi], r.weights[lo:hi], renormalize=renorm)
+            assert torch.equal(d[lo:hi], part)
+
+
 def test_sort_of_many_slots():
     """More slots than 256 groups of 65535 hold."""
     m, rng = _m(), np.random.default_rng(3)
