@@ -129,8 +129,11 @@ int64_t mx_moe_workspace(int64_t tokens, int32_t num_experts, int32_t topk);
  * mx_moe_combine_backward name one row, either is left there, or a mixture.
  *
  * mx_moe_dispatch -- rows[row_of[t, j]] = x[t], BF16.  (The products gather by row_token
- * themselves; this is for what needs the rows in memory, as the columnwise copy of
- * a weight gradient.)  Its gradient is mx_moe_combine of the rows' gradients with weights NULL.
+ * themselves; this is for what needs the rows in memory: a BF16 or rowwise
+ * quantized operand, products of one expert's rows at a time.  Experts' ranges start
+ * at any row, so a block of 16 rows or more of a columnwise or tile copy may hold rows of two
+ * experts: such a copy is no operand of a weight gradient per expert.)  Its gradient is
+ * mx_moe_combine of the rows' gradients with weights NULL.
  *
  * mx_moe_combine -- out[t] = sum over j of weights[t, j] rows[row_of[t, j]], in
  * binary32 in the order of j, one rounding to BF16; weights NULL: ones.  A token

@@ -472,7 +472,7 @@ void plan_moe(MoeArgs& a, bool routed) {
   a.groups = 0;
   a.group_tokens = a.T;
   const int lanes = lanes_of(a.E, a.k);
-  // one workgroup routes its pass of tokens, or sorts some slots (512 slots 3.6 us, 4096 9.8, where two launches take 7.2)
+  // one workgroup routes its pass of tokens, or sorts some slots (512 slots 3.6 us, 4096 9.8, where two launches take 7.1)
   if (routed ? a.T <= one_tokens(lanes) : a.T * a.k <= 2048) return;
   // at least a pass of the router's workgroup; up to 256 groups beyond that, while counts fit 16 bits
   const int64_t pass = lanes == 16 ? 32 : 16;

@@ -306,7 +306,9 @@ def _row_of(row_of, T, dev):
 def mx_moe_dispatch(x, row_of, num_rows=None, out=None):
     """rows[row_of[t, j]] = x[t] for the BF16 rows x [tokens, cols]: the experts'
     rows [num_rows, cols] in memory (num_rows: tokens * topk).  Rows that no
-    slot names are left as they were.  Its gradient is mx_moe_combine(drows, row_of)."""
+    slot names are left as they were: in a new tensor they hold anything, NaN included, so where slots
+    have no row and a later step reads every row (a second scale per tensor), pass zeros as
+    out.  Its gradient is mx_moe_combine(drows, row_of)."""
     T, cols, dev = _first(x, "x")
     ld_x = _matrix(x, "x", T, cols, dev)
     _, k = _row_of(row_of, T, dev)
@@ -339,7 +341,8 @@ def mx_moe_combine(rows, row_of, weights=None, out=None):
 def mx_moe_combine_backward(dout, rows, row_of, weights, drows=None, dweights=None):
     """Gradient of mx_moe_combine: (drows like rows, dweights float32 [tokens,
     topk]) from dout [tokens, cols].  Rows of drows that no slot names are left
-    as they were."""
+    as they were, and hold anything in a new tensor; their gradient is zero: pass zeros as drows
+    where a later step reads every row."""
     T, cols, dev = _first(dout, "dout")
     ld_d = _matrix(dout, "dout", T, cols, dev)
     M = rows.shape[0] if isinstance(rows, torch.Tensor) and rows.dim() else 0
